@@ -1,0 +1,432 @@
+"""The paged-cache operators on real work: what a serving step calls around the sparse branch.
+
+Four operators, each in a plain form (elementary torch operations in fp32) and
+as the framework's call (where `own` is true):
+
+  append   K, V and index keys of the step's new tokens into the pages (bf16 or int8 with scales)
+  gather   cached rows read back as packed bf16
+  attn     a chunk of new tokens (or one token) over the pages: causal, or a window with sinks
+  sparse   a decode step of the sparse branch over int8 pages
+
+A step of a batch is described by cu [Bt + 1] (first packed row of each
+sequence) and kv_len [Bt] (its context length, the new tokens included): row i
+of sequence b stands at position kv_len[b] - n_b + i.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+
+# ------------------------------------------------------------------ the cases
+def listed():
+    return [
+        # one decode step's new tokens of a serving batch: pure latency
+        dict(name="append_i8_step", op="append", i8=True, Bt=64, n=1, T=2048, Hkv=8, d=128,
+             block=128, d_idx=128),
+        # prompts of three requests entering an int8 cache
+        dict(name="append_i8_prompts", op="append", i8=True, Bt=3, n=8191, T=9001, Hkv=8, d=128,
+             block=128, d_idx=128),
+        # a chunk of odd lengths into a raw cache with small heads
+        dict(name="append_bf16_chunk", op="append", i8=False, Bt=4, n=1025, T=5003, Hkv=2, d=64,
+             block=64, d_idx=64),
+        # a whole long context read back for a contiguous prefill call
+        dict(name="gather_i8_long", op="gather", i8=True, Bt=1, n=131072, T=131072, Hkv=8, d=128,
+             block=512),
+        # tails of a few raw contexts
+        dict(name="gather_bf16_tails", op="gather", i8=False, Bt=5, n=1777, T=8192, Hkv=8, d=128,
+             block=64),
+        # one user, one token, a small model: the smallest call
+        dict(name="attn_one_token", op="attn", i8=False, Bt=1, n=1, T=4001, Hq=8, Hkv=2, d=64,
+             block=64, window=0, sinks=0),
+        # a decode batch with contexts of all lengths over an int8 cache
+        dict(name="attn_decode_i8_32", op="attn", i8=True, Bt=32, n=1, T=32768, Hq=64, Hkv=8,
+             d=128, block=128, window=0, sinks=0),
+        # a prefill chunk deep in a context, dense
+        dict(name="attn_chunk_bf16", op="attn", i8=False, Bt=1, n=2048, T=32768, Hq=32, Hkv=8,
+             d=128, block=128, window=0, sinks=0),
+        # a mixed batch: chunks and single tokens over an int8 cache
+        dict(name="attn_mixed_i8", op="attn", i8=True, Bt=6, n=701, T=12007, Hq=64, Hkv=8, d=128,
+             block=512, window=0, sinks=0),
+        # a prompt through a layer with a window and first tokens that stay
+        dict(name="attn_window_prompt", op="attn", i8=False, Bt=1, n=8192, T=8192, Hq=32, Hkv=8,
+             d=128, block=128, window=1024, sinks=4),
+        # the sparse branch of the 32 x 128K decode step on int8 pages
+        dict(name="sparse_i8_32x131072", op="sparse", i8=True, Bt=32, n=1, T=131072, Hq=64, Hkv=8,
+             d=128, block=128, K=16),
+        # the same for a few short contexts of a small model
+        dict(name="sparse_i8_small", op="sparse", i8=True, Bt=3, n=1, T=5000, Hq=8, Hkv=2, d=64,
+             block=64, K=8),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["append", "gather", "attn", "attn", "attn", "sparse"])
+    d = rng.choice([64, 128])
+    Hkv = rng.choice([1, 2, 4, 8])
+    block = rng.choice([32, 64, 128, 128, 256, 512])
+    i8 = rng.random() < 0.5
+    if op in ("append", "gather"):
+        Bt = _log(rng, 1, 48)
+        n = min(_log(rng, 1, 16384), 32768 // Bt)
+        c = dict(op=op, i8=i8, Bt=Bt, n=n, T=n + _log(rng, 1, 2048), Hkv=Hkv, d=d, block=block)
+        if op == "append":
+            c["d_idx"] = rng.choice([0, 64, 128])
+        return c
+    Hq = Hkv * rng.choice([1, 2, 4, 8, 16])
+    if op == "sparse":
+        Bt = _log(rng, 1, 32)
+        return dict(op=op, i8=True, Bt=Bt, n=1, T=min(_log(rng, 100, 131072), (1 << 21) // Bt),
+                    Hq=Hq, Hkv=Hkv, d=d, block=block, K=rng.choice([1, 4, 8, 13, 16]))
+    window = rng.choice([0, 0, _log(rng, 16, 4096)])
+    sinks = rng.choice([0, 1, 4, 64]) if window else 0
+    Bt = _log(rng, 1, 32)
+    n = 1 if rng.random() < 0.4 else min(_log(rng, 2, 4096), 4096 // Bt)
+    # the plain form holds all scores: at most 2^29 of them
+    T = n + min(_log(rng, 16, 32768), (1 << 29) // (Bt * max(n, 1) * Hq))
+    return dict(op=op, i8=i8, Bt=Bt, n=n, T=T, Hq=Hq, Hkv=Hkv, d=d, block=block, window=window,
+                sinks=sinks)
+
+
+def _lengths(c):
+    """New tokens and context length of each sequence: the first has the
+    case's n and T, the others spread below them (whole-number arithmetic of
+    the case alone)."""
+    r = random.Random(1000003 * c["Bt"] + 1009 * c["T"] + c["n"])
+    ns, ts = [c["n"]], [c["T"]]
+    for b in range(1, c["Bt"]):
+        n = max(1, int(c["n"] * r.random()))
+        ns.append(n)
+        ts.append(c["T"] if c["op"] == "sparse" else n + int((c["T"] - c["n"]) * r.random()))
+    return ns, ts
+
+
+# ------------------------------------------------------------------ the inputs
+def _normal(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda", dtype=torch.float32).to(torch.bfloat16)
+
+
+def _store(g, pages, block, Hkv, d, i8):
+    """A page store in use: bf16 values, or int8 codes with the scales
+    [pages, Hkv, block] of rows whose largest value is about 2 to 4."""
+    if not i8:
+        return torch.randn((pages, block, Hkv, d), generator=g, device="cuda",
+                           dtype=torch.bfloat16), None
+    codes = torch.empty((pages, block, Hkv, d), dtype=torch.int8, device="cuda")
+    step = max(1, (1 << 27) // (block * Hkv * d))
+    for p in range(0, pages, step):
+        part = codes[p:p + step]
+        x = torch.randn(part.shape, generator=g, device="cuda", dtype=torch.bfloat16)
+        part.copy_(x.mul_(42).round_().clamp_(-127, 127))
+    scales = (2 + 2 * torch.rand((pages, Hkv, block), generator=g, device="cuda")) / 127
+    return codes, scales
+
+
+def prepare(case, seed):
+    c = dict(case)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    ns, ts = _lengths(c)
+    Bt, Hkv, d, block = c["Bt"], c["Hkv"], c["d"], c["block"]
+    per = [-(-t // block) for t in ts]
+    pages, width = sum(per) + 2, max(per)
+    order = torch.randperm(pages, generator=g, device="cuda").to(torch.int32).cpu()
+    table = torch.zeros((Bt, width), dtype=torch.int32)
+    at = 0
+    for b in range(Bt):
+        table[b, :per[b]] = order[at:at + per[b]]
+        at += per[b]
+    cu = [0]
+    for n in ns:
+        cu.append(cu[-1] + n)
+    s = dict(case=c, total=cu[-1], n_max=max(ns), t_max=max(ts), table=table.cuda(),
+             cu=torch.tensor(cu, dtype=torch.int32).cuda(),
+             kv_len=torch.tensor(ts, dtype=torch.int32).cuda())
+    s["k_pages"], s["k_scales"] = _store(g, pages, block, Hkv, d, c["i8"])
+    s["v_pages"], s["v_scales"] = _store(g, pages, block, Hkv, d, c["i8"])
+    if c["op"] == "append":
+        # keys with a few strong channels, as projections give them
+        strong = 1 + 3 * (torch.rand(d, generator=g, device="cuda") < 0.05)
+        s["k"] = (_normal(g, cu[-1], Hkv, d) * strong).to(torch.bfloat16)
+        s["v"] = _normal(g, cu[-1], Hkv, d)
+        if c["d_idx"]:
+            s["k_idx"] = torch.randint(-3, 4, (cu[-1], c["d_idx"]), generator=g,
+                                       device="cuda").to(torch.bfloat16)
+            s["k_idx_pages"] = torch.zeros((pages, block, c["d_idx"]), dtype=torch.bfloat16,
+                                           device="cuda")
+    if c["op"] == "attn":
+        s["q"] = _normal(g, cu[-1], c["Hq"], d)
+    if c["op"] == "sparse":
+        s["q"] = _normal(g, Bt, 1, c["Hq"], d)
+        N = -(-c["T"] // block)
+        K = c["K"]
+        # the own block and distinct others, ascending, -1 behind them
+        pick = torch.rand((Bt, N), generator=g, device="cuda")
+        pick[:, N - 1] = 2
+        ids = pick.topk(min(K, N), dim=1).indices.sort(dim=1).values.to(torch.int32)
+        pad = torch.full((Bt, K - ids.shape[1]), -1, dtype=torch.int32, device="cuda")
+        s["ids"] = torch.cat([ids, pad], dim=1).reshape(Bt, 1, K).contiguous()
+    if own:  # the scratch buffer that a program of the framework keeps beside its cache
+        from block_sparse_long_05_b200 import msa
+        s["ws"] = msa.Workspace.for_cache(c.get("Hq", Hkv), Hkv, d)
+    return s
+
+
+# ------------------------------------------------------------------ the plain forms
+def _rows(s):
+    """Sequence, page and row in the page of each packed row."""
+    i = torch.arange(s["total"], device="cuda")
+    b = (i[:, None] >= s["cu"][None, 1:]).sum(1)
+    pos = s["kv_len"][b] - s["cu"][b + 1] + i
+    return s["table"][b, pos // s["case"]["block"]].long(), pos % s["case"]["block"]
+
+
+def _quantise(x):
+    x = x.float()
+    amax = x.abs().amax(-1)
+    inv = torch.where(amax > 0, 127 / amax, torch.zeros_like(amax))
+    return (x * inv[..., None]).round().to(torch.int8), amax / 127
+
+
+def _plain_append(s):
+    page, row = _rows(s)
+    for x, pages, scales in ((s["k"], s["k_pages"], s["k_scales"]),
+                             (s["v"], s["v_pages"], s["v_scales"])):
+        if scales is None:
+            pages[page, row] = x
+        else:
+            codes, scale = _quantise(x)
+            pages[page, row] = codes
+            scales[page, :, row] = scale
+    if "k_idx" in s:
+        s["k_idx_pages"][page, row] = s["k_idx"]
+
+
+def _plain_gather(s):
+    page, row = _rows(s)
+    if not s["case"]["i8"]:
+        return s["k_pages"][page, row], s["v_pages"][page, row]
+    k = s["k_pages"][page, row].float() * s["k_scales"][page, :, row][..., None]
+    v = s["v_pages"][page, row].float() * s["v_scales"][page, :, row][..., None]
+    return k.to(torch.bfloat16), v.to(torch.bfloat16)
+
+
+def _cached(pages, scales, index):
+    """[Bt, Hkv, keys, d] fp32 of the pages index [Bt, blocks]."""
+    x = pages[index].float()
+    if scales is not None:
+        x *= scales[index].transpose(2, 3)[..., None]
+    return x.flatten(1, 2).transpose(1, 2)
+
+
+def _softmax_product(q, k, v, seen):
+    """q [Bt, Hkv, rows, d], k / v [Bt, Hkv, keys, d], seen [Bt, 1, rows, keys]."""
+    s = q @ k.transpose(2, 3)
+    s *= 1 / math.sqrt(q.shape[-1])
+    s.masked_fill_(~seen, -math.inf)
+    top = s.amax(-1, keepdim=True)
+    p = s.sub_(top).exp_()
+    total = p.sum(-1, keepdim=True)
+    return (p @ v) / total, (top + total.log()).squeeze(-1)
+
+
+def _plain_attn(s):
+    c = s["case"]
+    G, Hkv, n, d = c["Hq"] // c["Hkv"], c["Hkv"], s["n_max"], c["d"]
+    index = s["table"].long()
+    k = _cached(s["k_pages"], s["k_scales"], index)[:, :, :s["t_max"]]
+    v = _cached(s["v_pages"], s["v_scales"], index)[:, :, :s["t_max"]]
+    i = torch.arange(n, device="cuda")
+    rows = (s["cu"][:-1, None] + i).clamp(max=s["total"] - 1)
+    q = s["q"].float()[rows].reshape(c["Bt"], n, Hkv, G, d).transpose(1, 2).flatten(2, 3)
+    own_n = s["cu"][1:] - s["cu"][:-1]
+    t = (s["kv_len"] - own_n)[:, None] + i
+    # rows behind a sequence's last one stand at its last position; they are not kept
+    t = torch.minimum(t, s["kv_len"][:, None] - 1)[:, :, None]
+    j = torch.arange(s["t_max"], device="cuda")
+    seen = j <= t
+    if c["window"]:
+        seen &= (j > t - c["window"]) | (j < c["sinks"])
+    seen = seen[:, None].repeat_interleave(G, 2)
+    # rows past the context hold nothing that may be used
+    v = torch.where((j < s["kv_len"][:, None])[:, None, :, None], v, torch.zeros_like(v))
+    o, lse = _softmax_product(q, k, v, seen)
+    o = o.unflatten(2, (n, G)).transpose(1, 2).flatten(2, 3)
+    lse = lse.unflatten(2, (n, G)).transpose(1, 2).flatten(2, 3)
+    a = torch.arange(s["total"], device="cuda")
+    b = (a[:, None] >= s["cu"][None, 1:]).sum(1)
+    return o[b, a - s["cu"][b]].to(torch.bfloat16), lse[b, a - s["cu"][b]]
+
+
+def _plain_sparse(s):
+    c = s["case"]
+    Bt, Hkv, d, block, K = c["Bt"], c["Hkv"], c["d"], c["block"], c["K"]
+    ids = s["ids"].reshape(Bt, K).long()
+    index = s["table"].long().gather(1, ids.clamp(min=0))
+    k = _cached(s["k_pages"], s["k_scales"], index)
+    v = _cached(s["v_pages"], s["v_scales"], index)
+    j = ids[:, :, None] * block + torch.arange(block, device="cuda")
+    seen = ((ids[:, :, None] >= 0) & (j < c["T"])).flatten(1)[:, None, None]
+    o, lse = _softmax_product(s["q"].float().reshape(Bt, Hkv, c["Hq"] // Hkv, d), k, v, seen)
+    return (o.reshape(Bt, 1, c["Hq"], d).to(torch.bfloat16), lse.reshape(Bt, 1, c["Hq"]))
+
+
+# ------------------------------------------------------------------ one pass
+def _stores(s):
+    """The cache after an append: codes are whole numbers, beside the scales
+    that make values of them."""
+    return {name: s[name] for name in ("k_pages", "v_pages", "k_scales", "v_scales",
+                                       "k_idx_pages") if s.get(name) is not None}
+
+
+def run(state):
+    s = state
+    c = s["case"]
+    if own:
+        from block_sparse_long_05_b200 import msa
+        step = (s["table"], s["cu"], s["kv_len"])
+        if c["op"] == "append":
+            index = dict(k_idx=s["k_idx"], k_idx_pages=s["k_idx_pages"]) if "k_idx" in s else {}
+            if c["i8"]:
+                msa.kv_append_i8(s["k"], s["v"], s["k_pages"], s["v_pages"], s["k_scales"],
+                                 s["v_scales"], *step, s["ws"], **index)
+            else:
+                msa.kv_append(s["k"], s["v"], s["k_pages"], s["v_pages"], *step, s["ws"], **index)
+            return _stores(s)
+        if c["op"] == "gather":
+            if c["i8"]:
+                return msa.kv_gather_i8(s["k_pages"], s["v_pages"], s["k_scales"], s["v_scales"],
+                                        *step, s["total"], s["ws"])
+            return msa.kv_gather(s["k_pages"], s["v_pages"], *step, s["total"], s["ws"])
+        if c["op"] == "attn":
+            how = dict(window=c["window"], sinks=c["sinks"], max_q=s["n_max"])
+            if c["i8"]:
+                return msa.attn_paged_i8(s["q"], s["k_pages"], s["v_pages"], s["k_scales"],
+                                         s["v_scales"], *step, s["ws"], **how)
+            return msa.attn_paged(s["q"], s["k_pages"], s["v_pages"], *step, s["ws"], **how)
+        return msa.sparse_attn_paged_i8(s["q"], s["k_pages"], s["v_pages"], s["k_scales"],
+                                        s["v_scales"], s["table"], c["T"], s["ids"], s["ws"])
+    if c["op"] == "append":
+        _plain_append(s)
+        return _stores(s)
+    if c["op"] == "gather":
+        return _plain_gather(s)
+    if c["op"] == "attn":
+        return _plain_attn(s)
+    return _plain_sparse(s)
+
+
+# ------------------------------------------------------------------ work and exact values
+def _seen_by(c, t):
+    """Keys that a query at position t sees."""
+    if not c["window"]:
+        return t + 1
+    near = min(c["window"], t + 1)
+    return near + min(c["sinks"], t + 1 - near)
+
+
+def work(case):
+    c = case
+    ns, ts = _lengths(c)
+    Hkv, d = c["Hkv"], c["d"]
+    row = Hkv * (2 * d + 8 if c["i8"] else 4 * d)  # K and V of one cached token, with scales
+    total = sum(ns)
+    if c["op"] == "append":
+        return {"bytes": total * (4 * Hkv * d + row + 4 * c["d_idx"]), "flops": 0}
+    if c["op"] == "gather":
+        return {"bytes": total * (4 * Hkv * d + row), "flops": 0}
+    q_out = total * c["Hq"] * (4 * d + 4)
+    if c["op"] == "sparse":
+        N = -(-c["T"] // c["block"])
+        keys = min(c["K"], N) * c["block"] - (N * c["block"] - c["T"])
+        return {"bytes": c["Bt"] * keys * row + q_out, "flops": 4 * d * c["Hq"] * c["Bt"] * keys}
+    pairs = keys = 0
+    for n, t in zip(ns, ts):
+        pairs += sum(_seen_by(c, t - n + i) for i in range(n))
+        # keys that any of the n queries sees
+        near = t if not c["window"] else min(t, c["window"] + n - 1)
+        keys += near + min(c["sinks"], t - near)
+    return {"bytes": keys * row + q_out, "flops": 4 * d * c["Hq"] * pairs}
+
+
+def _exact_context(s, b, upto):
+    """K and V of sequence b in 64 bits, page by page: [upto, Hkv, d]."""
+    got = []
+    block = s["case"]["block"]
+    pages = [int(p) for p in s["table"][b, :-(-upto // block)].cpu()]
+    for store, scales in ((s["k_pages"], s["k_scales"]), (s["v_pages"], s["v_scales"])):
+        x = torch.cat([store[p] for p in pages]).double()
+        if scales is not None:
+            x = x * torch.cat([scales[p].t() for p in pages]).double()[:, :, None]
+        got.append(x[:upto])
+    return got
+
+
+def _exact_head(q, k, v, seen):
+    z = (q @ k.t()) / math.sqrt(k.shape[1])
+    z = torch.where(seen, z, torch.full_like(z, -math.inf))
+    lse = torch.logsumexp(z, 1)
+    return torch.exp(z - lse[:, None]) @ v, lse
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    c = s["case"]
+    ns, ts = _lengths(c)
+    block = c["block"]
+    if c["op"] == "append":
+        # a run of one page at a time; int8 codes are whole numbers and have no 64-bit value
+        new = {"k_pages": "k", "v_pages": "v"} if not c["i8"] else {"k_scales": "k",
+                                                                   "v_scales": "v"}
+        if c["d_idx"]:
+            new["k_idx_pages"] = "k_idx"
+        got, at = {name: s[name].double() for name in new}, 0
+        for b, (n, t) in enumerate(zip(ns, ts)):
+            pos = t - n
+            while pos < t:
+                m, r = min(t - pos, block - pos % block), pos % block
+                page = int(s["table"][b, pos // block])
+                for name in new:
+                    x = s[new[name]][at:at + m].double()
+                    if name.endswith("scales"):
+                        got[name][page, :, r:r + m] = (x.abs().max(2).values / 127).t()
+                    else:
+                        got[name][page, r:r + m] = x
+                pos, at = pos + m, at + m
+        return got
+    if c["op"] == "gather":
+        parts = [[x[t - n:] for x in _exact_context(s, b, t)]
+                 for b, (n, t) in enumerate(zip(ns, ts))]
+        return torch.cat([p[0] for p in parts]), torch.cat([p[1] for p in parts])
+    G = c["Hq"] // c["Hkv"]
+    o = torch.zeros(s["q"].shape, dtype=torch.float64, device="cuda")
+    lse = torch.zeros(s["q"].shape[:-1], dtype=torch.float64, device="cuda")
+    if c["op"] == "sparse":
+        for b in range(c["Bt"]):
+            ids = [int(x) for x in s["ids"][b, 0].cpu() if x >= 0]
+            part = dict(s, table=s["table"][b:b + 1, ids])
+            k, v = _exact_context(part, 0, len(ids) * block)
+            last = len(ids) * block - (ids[-1] + 1) * block + c["T"] if ids else 0
+            seen = torch.arange(len(ids) * block, device="cuda")[None] < min(last, len(ids) * block)
+            for h in range(c["Hq"]):
+                x, y = _exact_head(s["q"][b, :, h].double(), k[:, h // G], v[:, h // G], seen)
+                o[b, :, h], lse[b, :, h] = x, y
+        return o, lse
+    at = 0
+    for b, (n, t) in enumerate(zip(ns, ts)):
+        k, v = _exact_context(s, b, t)
+        i = torch.arange(t - n, t, device="cuda")[:, None]
+        j = torch.arange(t, device="cuda")[None]
+        seen = j <= i
+        if c["window"]:
+            seen = seen & ((i - j < c["window"]) | (j < c["sinks"]))
+        for h in range(c["Hq"]):
+            x, y = _exact_head(s["q"][at:at + n, h].double(), k[:, h // G], v[:, h // G], seen)
+            o[at:at + n, h], lse[at:at + n, h] = x, y
+        at += n
+    return o, lse
