@@ -189,8 +189,10 @@ def _rows(s):
 def _quantise(x):
     x = x.float()
     amax = x.abs().amax(-1)
-    inv = torch.where(amax > 0, 127 / amax, torch.zeros_like(amax))
-    return (x * inv[..., None]).round().to(torch.int8), amax / 127
+    # tensors on both sides: a division by a plain number multiplies by its reciprocal
+    most = torch.full_like(amax, 127)
+    inv = torch.where(amax > 0, most / amax, torch.zeros_like(amax))
+    return (x * inv[..., None]).round().to(torch.int8), amax / most
 
 
 def _plain_append(s):
