@@ -11,6 +11,7 @@
 #include "../../include/msa.h"
 #include "kernels.h"
 #include "msa_common.cuh"
+#include "tmap.h"
 
 using namespace msa;
 
@@ -126,52 +127,6 @@ T *at(void *ws, size_t off) {
 }
 
 msa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA; }
-
-int num_sms_current() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return n;
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn load_encode() {
-    void *fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-        return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(fn);
-}
-
-EncodeTiledFn encode_fn() {
-    static const EncodeTiledFn fn = load_encode();  // thread-safe one-time init
-    return fn;
-}
-
-// Tensor map (bf16 by default, or bytes) with 128-byte swizzle (or 64-byte
-// for 64-byte box rows); dims/strides innermost first (strides in bytes for
-// dims 1..rank-1).
-bool make_tmap(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims,
-               const cuuint64_t *strides, const cuuint32_t *box,
-               CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-               CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = fn(m, dtype, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims,
-                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 // Record the start/stop event of stage i (if the caller supplied one).
 void mark(const msa_stage_events *ev, int i, bool start, cudaStream_t st) {

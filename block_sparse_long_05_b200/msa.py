@@ -28,7 +28,9 @@ EXPORTED = ("msa_workspace_size", "msa_index_topk", "msa_select_invert", "msa_sp
             "msa_index_topk_ev", "msa_sparse_attn_ev", "msa_device_status", "msa_status_string",
             "msa_selftest_umma", "msa_sparse_attn_decode_noalloc", "msa_index_topk_paged",
             "msa_sparse_attn_paged", "msa_index_topk_i8", "msa_index_topk_i8_ev",
-            "msa_workspace_size_kv_group")
+            "msa_workspace_size_kv_group", "msa_cache_workspace_size", "msa_kv_append",
+            "msa_kv_append_i8", "msa_kv_gather", "msa_kv_gather_i8", "msa_attn_paged",
+            "msa_attn_paged_i8", "msa_sparse_attn_paged_i8")
 
 MAX_STAGES = 4
 
@@ -103,6 +105,23 @@ def load_library(path: str = LIB_PATH):
     lib.msa_index_topk_paged.restype = I
     lib.msa_sparse_attn_paged.argtypes = [P, P, P, P, I, I, P, P, P, I, I, I, I, I, I, I, P, Z, P]
     lib.msa_sparse_attn_paged.restype = I
+    L = ctypes.c_int64
+    lib.msa_cache_workspace_size.argtypes = [I, I, I]
+    lib.msa_cache_workspace_size.restype = Z
+    step = [P, I, I, P, P]  # page_table, page_stride, num_pages, cu, kv_len
+    lib.msa_kv_append.argtypes = [P, L, P, L, P, L, P, P, P, *step, I, I, I, I, I, I, P, Z, P]
+    lib.msa_kv_append_i8.argtypes = [P, L, P, L, P, L, P, P, P, P, P, *step, I, I, I, I, I, I, P, Z,
+                                     P]
+    lib.msa_kv_gather.argtypes = [P, P, *step, P, P, I, I, I, I, I, P, Z, P]
+    lib.msa_kv_gather_i8.argtypes = [P, P, P, P, *step, P, P, I, I, I, I, I, P, Z, P]
+    lib.msa_attn_paged.argtypes = [P, L, P, P, *step, P, P, I, I, I, I, I, I, I, I, I, P, Z, P]
+    lib.msa_attn_paged_i8.argtypes = [P, L, P, P, P, P, *step, P, P, I, I, I, I, I, I, I, I, I, P, Z,
+                                      P]
+    lib.msa_sparse_attn_paged_i8.argtypes = [P, P, P, P, P, P, I, I, P, P, P, I, I, I, I, I, I, I, P,
+                                             Z, P]
+    for f in ("kv_append", "kv_append_i8", "kv_gather", "kv_gather_i8", "attn_paged",
+              "attn_paged_i8", "sparse_attn_paged_i8"):
+        getattr(lib, "msa_" + f).restype = I
     lib.msa_selftest_umma.argtypes = [P, P, P, I, I, I, P, P]
     lib.msa_selftest_umma.restype = I
     _lib = lib
@@ -160,6 +179,11 @@ class Workspace:
     def for_shape(cls, Bt, n_q, T, Hq, Hkv, d, d_idx, block, K, device=None,
                   kv_group=None) -> "Workspace":
         return cls(workspace_size(Bt, n_q, T, Hq, Hkv, d, d_idx, block, K, kv_group), device)
+
+    @classmethod
+    def for_cache(cls, Hq, Hkv, d, device=None) -> "Workspace":
+        """Workspace of the paged-cache calls (kv_append .. sparse_attn_paged_i8)."""
+        return cls(int(load_library().msa_cache_workspace_size(Hq, Hkv, d)), device)
 
 
 def index_topk(q_idx: torch.Tensor, k_idx: torch.Tensor, block: int, K: int, ws: Workspace,
@@ -336,6 +360,245 @@ def sparse_attn_decode_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
                                               ids.data_ptr(), out.data_ptr(), lse.data_ptr(), Bt,
                                               T, Hq, Hkv, d, block, K, sp or None,
                                               _stream(stream)))
+    return out, lse
+
+
+class _Call:
+    """Device and stream of a paged-cache call: every tensor must live on one
+    device, which is made current for the launch; the stream defaults to that
+    device's current one."""
+
+    def __init__(self, ws: Workspace, stream, **tensors):
+        self.device = ws.view.device
+        for name, t in tensors.items():
+            if t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, the workspace on {self.device}")
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        self.stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+    def __call__(self, fn: str, *args):
+        call = getattr(load_library(), fn)
+        if self.device.index == torch.cuda.current_device():
+            _check(fn, call(*args, self.stream))
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn, call(*args, self.stream))
+
+
+def _rows(t: torch.Tensor, name: str, dims: int) -> int:
+    """Elements between the rows of a packed bf16 tensor whose rows are contiguous."""
+    if t.dtype != torch.bfloat16 or t.dim() != dims:
+        raise ValueError(f"{name} must be a bfloat16 tensor of {dims} dimensions")
+    width = 1
+    for i in range(dims - 1, 0, -1):
+        if t.shape[i] != 1 and t.stride(i) != width:
+            raise ValueError(f"{name}: each row must be contiguous")
+        width *= t.shape[i]
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _stores(k_pages, v_pages, k_scales=None, v_scales=None):
+    """(num_pages, block, Hkv, d) of a checked pair of page stores."""
+    dtype = torch.bfloat16 if k_scales is None else torch.int8
+    _dev(k_pages, dtype, "k_pages")
+    _dev(v_pages, dtype, "v_pages")
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must be [num_pages, block, Hkv, d]")
+    if k_scales is not None:
+        pages, block, Hkv, _ = k_pages.shape
+        for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _dev(t, torch.float32, name)
+            if t.shape != (pages, Hkv, block):
+                raise ValueError(f"{name} must be [num_pages, Hkv, block]")
+    return k_pages.shape
+
+
+def _step(page_table, cu, kv_len) -> int:
+    """Bt of a checked step description."""
+    _dev(page_table, torch.int32, "page_table")
+    _dev(cu, torch.int32, "cu")
+    _dev(kv_len, torch.int32, "kv_len")
+    Bt = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    if page_table.dim() != 2 or page_table.shape[0] != Bt or cu.shape != (Bt + 1,):
+        raise ValueError("page_table must be [Bt, page_stride], cu [Bt + 1], kv_len [Bt]")
+    return Bt
+
+
+def _append(fn, k, v, k_pages, v_pages, scales, page_table, cu, kv_len, ws, k_idx, k_idx_pages,
+            stream):
+    num_pages, block, Hkv, d = _stores(k_pages, v_pages, *scales)
+    Bt = _step(page_table, cu, kv_len)
+    ks, vs = _rows(k, "k", 3), _rows(v, "v", 3)
+    if k.shape != v.shape or k.shape[1:] != (Hkv, d):
+        raise ValueError("k and v must be [total, Hkv, d]")
+    total, d_idx, xs, xp, xpp = k.shape[0], 0, 0, None, None
+    on = dict(k=k, v=v, k_pages=k_pages, v_pages=v_pages, page_table=page_table, cu=cu,
+              kv_len=kv_len)
+    if scales:
+        on.update(k_scales=scales[0], v_scales=scales[1])
+    if (k_idx is None) != (k_idx_pages is None):
+        raise ValueError("k_idx and k_idx_pages go together")
+    if k_idx is not None:
+        _dev(k_idx_pages, torch.bfloat16, "k_idx_pages")
+        xs, d_idx = _rows(k_idx, "k_idx", 2), k_idx.shape[1]
+        if k_idx.shape[0] != total or k_idx_pages.shape != (num_pages, block, d_idx):
+            raise ValueError("k_idx must be [total, d_idx], k_idx_pages [num_pages, block, d_idx]")
+        on.update(k_idx=k_idx, k_idx_pages=k_idx_pages)
+        xp, xpp = k_idx.data_ptr(), k_idx_pages.data_ptr()
+    run = _Call(ws, stream, **on)
+    if total:  # (a step without rows has nothing to write, and no pointers to check)
+        run(fn, k.data_ptr(), ks, v.data_ptr(), vs, xp, xs, k_pages.data_ptr(), v_pages.data_ptr(),
+            *(t.data_ptr() for t in scales), xpp, page_table.data_ptr(), page_table.shape[1],
+            num_pages, cu.data_ptr(), kv_len.data_ptr(), Bt, total, Hkv, d, d_idx, block, ws.ptr,
+            ws.nbytes)
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+              page_table: torch.Tensor, cu: torch.Tensor, kv_len: torch.Tensor, ws: Workspace,
+              k_idx: torch.Tensor | None = None, k_idx_pages: torch.Tensor | None = None,
+              stream=None) -> None:
+    """A step's new rows into the pages (msa_kv_append): k, v [total, Hkv, d] bf16 (rows
+    may be strided), k_pages / v_pages [num_pages, block, Hkv, d] bf16, page_table
+    [Bt, page_stride], cu [Bt + 1], kv_len [Bt] int32; optionally the index keys k_idx
+    [total, d_idx] into k_idx_pages [num_pages, block, d_idx]."""
+    _append("msa_kv_append", k, v, k_pages, v_pages, (), page_table, cu, kv_len, ws, k_idx,
+            k_idx_pages, stream)
+
+
+def kv_append_i8(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 k_scales: torch.Tensor, v_scales: torch.Tensor, page_table: torch.Tensor,
+                 cu: torch.Tensor, kv_len: torch.Tensor, ws: Workspace,
+                 k_idx: torch.Tensor | None = None, k_idx_pages: torch.Tensor | None = None,
+                 stream=None) -> None:
+    """kv_append into int8 pages with a scale per (token, kv head) row
+    (msa_kv_append_i8): k_scales / v_scales [num_pages, Hkv, block] fp32."""
+    _append("msa_kv_append_i8", k, v, k_pages, v_pages, (k_scales, v_scales), page_table, cu,
+            kv_len, ws, k_idx, k_idx_pages, stream)
+
+
+def _gather(fn, k_pages, v_pages, scales, page_table, cu, kv_len, total, ws, k, v, stream):
+    num_pages, block, Hkv, d = _stores(k_pages, v_pages, *scales)
+    Bt = _step(page_table, cu, kv_len)
+    if k is None:
+        k = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=k_pages.device)
+    if v is None:
+        v = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=k_pages.device)
+    _dev(k, torch.bfloat16, "k")
+    _dev(v, torch.bfloat16, "v")
+    if k.shape != (total, Hkv, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [total, Hkv, d]")
+    on = dict(k=k, v=v, k_pages=k_pages, v_pages=v_pages, page_table=page_table, cu=cu,
+              kv_len=kv_len)
+    if scales:
+        on.update(k_scales=scales[0], v_scales=scales[1])
+    run = _Call(ws, stream, **on)
+    if total:
+        run(fn, k_pages.data_ptr(), v_pages.data_ptr(), *(t.data_ptr() for t in scales),
+            page_table.data_ptr(), page_table.shape[1], num_pages, cu.data_ptr(),
+            kv_len.data_ptr(), k.data_ptr(), v.data_ptr(), Bt, total, Hkv, d, block, ws.ptr,
+            ws.nbytes)
+    return k, v
+
+
+def kv_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+              cu: torch.Tensor, kv_len: torch.Tensor, total: int, ws: Workspace,
+              k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """Cached rows of a step's positions as packed bf16 (msa_kv_gather):
+    -> (k, v) [total, Hkv, d].  Rows behind cu[Bt] are left as they were."""
+    return _gather("msa_kv_gather", k_pages, v_pages, (), page_table, cu, kv_len, total, ws, k, v,
+                   stream)
+
+
+def kv_gather_i8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
+                 v_scales: torch.Tensor, page_table: torch.Tensor, cu: torch.Tensor,
+                 kv_len: torch.Tensor, total: int, ws: Workspace, k: torch.Tensor | None = None,
+                 v: torch.Tensor | None = None, stream=None):
+    """kv_gather from int8 pages (msa_kv_gather_i8): code * scale, rounded once."""
+    return _gather("msa_kv_gather_i8", k_pages, v_pages, (k_scales, v_scales), page_table, cu,
+                   kv_len, total, ws, k, v, stream)
+
+
+def _outputs(q, shape, out, lse):
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+    _dev(out, torch.bfloat16, "out")
+    _dev(lse, torch.float32, "lse")
+    if out.shape != shape or lse.shape != shape[:-1]:
+        raise ValueError("out / lse shapes do not match q")
+    return out, lse
+
+
+def _attend(fn, q, k_pages, v_pages, scales, page_table, cu, kv_len, ws, window, sinks, max_q, out,
+            lse, stream):
+    num_pages, block, Hkv, d = _stores(k_pages, v_pages, *scales)
+    Bt = _step(page_table, cu, kv_len)
+    q_stride = _rows(q, "q", 3)
+    total, Hq, d2 = q.shape
+    if d2 != d:
+        raise ValueError("q must be [total, Hq, d]")
+    out, lse = _outputs(q, q.shape, out, lse)
+    on = dict(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, cu=cu, kv_len=kv_len,
+              out=out, lse=lse)
+    if scales:
+        on.update(k_scales=scales[0], v_scales=scales[1])
+    run = _Call(ws, stream, **on)
+    if total:
+        run(fn, q.data_ptr(), q_stride, k_pages.data_ptr(), v_pages.data_ptr(),
+            *(t.data_ptr() for t in scales), page_table.data_ptr(), page_table.shape[1], num_pages,
+            cu.data_ptr(), kv_len.data_ptr(), out.data_ptr(), lse.data_ptr(), Bt, total, max_q or 0,
+            Hq, Hkv, d, block, window, sinks, ws.ptr, ws.nbytes)
+    return out, lse
+
+
+def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+               page_table: torch.Tensor, cu: torch.Tensor, kv_len: torch.Tensor, ws: Workspace,
+               window: int = 0, sinks: int = 0, max_q: int | None = None,
+               out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+    """Attention of a step's rows over their cached contexts (msa_attn_paged): q
+    [total, Hq, d] bf16 (rows may be strided) over k_pages / v_pages
+    [num_pages, block, Hkv, d] bf16 -> (out [total, Hq, d] bf16, lse [total, Hq] fp32).
+    window > 0: each query sees the last `window` keys and the first `sinks` ones.
+    max_q: the largest number of rows of one sequence, if known (it chooses kernels)."""
+    return _attend("msa_attn_paged", q, k_pages, v_pages, (), page_table, cu, kv_len, ws, window,
+                   sinks, max_q, out, lse, stream)
+
+
+def attn_paged_i8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                  k_scales: torch.Tensor, v_scales: torch.Tensor, page_table: torch.Tensor,
+                  cu: torch.Tensor, kv_len: torch.Tensor, ws: Workspace, window: int = 0,
+                  sinks: int = 0, max_q: int | None = None, out: torch.Tensor | None = None,
+                  lse: torch.Tensor | None = None, stream=None):
+    """attn_paged over int8 pages with their scales (msa_attn_paged_i8)."""
+    return _attend("msa_attn_paged_i8", q, k_pages, v_pages, (k_scales, v_scales), page_table, cu,
+                   kv_len, ws, window, sinks, max_q, out, lse, stream)
+
+
+def sparse_attn_paged_i8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                         k_scales: torch.Tensor, v_scales: torch.Tensor, page_table: torch.Tensor,
+                         T: int, ids: torch.Tensor, ws: Workspace, out: torch.Tensor | None = None,
+                         lse: torch.Tensor | None = None, stream=None):
+    """Decode sparse branch over int8 pages (msa_sparse_attn_paged_i8): q [Bt, 1, Hq, d]
+    bf16, ids [Bt, 1, K] int32 -> (out [Bt, 1, Hq, d] bf16, lse [Bt, 1, Hq] fp32).  ws is
+    a cache workspace (Workspace.for_cache)."""
+    num_pages, block, Hkv, d = _stores(k_pages, v_pages, k_scales, v_scales)
+    _dev(q, torch.bfloat16, "q")
+    _dev(page_table, torch.int32, "page_table")
+    _dev(ids, torch.int32, "ids")
+    Bt, n_q, Hq, d2 = q.shape
+    K = ids.shape[-1]
+    if n_q != 1 or d2 != d or ids.shape != (Bt, 1, K) or page_table.dim() != 2 or \
+            page_table.shape[0] != Bt:
+        raise ValueError("paged attention: shapes do not match")
+    out, lse = _outputs(q, q.shape, out, lse)
+    run = _Call(ws, stream, q=q, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales,
+                v_scales=v_scales, page_table=page_table, ids=ids, out=out, lse=lse)
+    run("msa_sparse_attn_paged_i8", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        k_scales.data_ptr(), v_scales.data_ptr(), page_table.data_ptr(), page_table.shape[1],
+        num_pages, ids.data_ptr(), out.data_ptr(), lse.data_ptr(), Bt, T, Hq, Hkv, d, block, K,
+        ws.ptr, ws.nbytes)
     return out, lse
 
 

@@ -195,6 +195,137 @@ MSA_API msa_status msa_sparse_attn_paged(const void *q, const void *k_pages, con
                                          size_t workspace_bytes, void *stream);
 
 /*
+ * Paged cache of a batch: writing it, reading it back, attending over it.
+ * ------------------------------------------------------------------------
+ * [P4 section 3.2] manages the KV cache in pages.  The calls below keep that
+ * cache (the page stores of msa_sparse_attn_paged, or 8-bit ones) and serve
+ * the layers around the sparse branch: dense attention of new tokens over
+ * their whole context, and attention in a window with first tokens that stay
+ * visible.  A step of a batch is described by two device arrays:
+ *   cu      [Bt + 1] int32: packed rows cu[b] .. cu[b+1]-1 belong to sequence
+ *           b (cu[0] = 0, ascending); rows at or behind cu[Bt] are neither
+ *           read nor written, so a padded buffer needs no copy;
+ *   kv_len  [Bt] int32: length of each context, this step's tokens included.
+ * Row i of the n_b = cu[b+1] - cu[b] rows of sequence b stands at position
+ * t = kv_len[b] - n_b + i.  The arrays are read when the kernels run: a
+ * captured step follows the lengths in them.  `total` is the number of rows
+ * that the packed buffers hold.  Where a row's position is negative, nothing
+ * is cached for it and it sees no key.
+ *
+ * Page stores: bf16 [num_pages][block][Hkv][d], or int8 codes of that shape
+ * with fp32 scales [num_pages][Hkv][block]: a cached row is code * scale.  As
+ * it is written, a row x of d values gets (all in fp32)
+ *     amax = max |x_i|, inv = 127 / amax, code_i = rint(x_i * inv), scale = amax / 127.
+ * Rows with amax < 2^-100 are stored as zeros; a row that holds an infinity
+ * or a NaN gets scale NaN, so that it reads back as NaN.
+ *
+ * Pages are found as in the paged decode calls above: logical block j of
+ * sequence b is page_table[b*page_stride + j].  A page id outside
+ * [0, num_pages), or a position that the table's row cannot hold, is skipped
+ * and reported as MSA_ERR_BAD_IDS in the status word (msa_device_status).
+ * Limits (MSA_ERR_UNSUPPORTED): d, d_idx in {64, 128}; block 32, 64 or a
+ * multiple of 128; num_pages*block < 2^31; page_stride*block, total < 2^30;
+ * total*Hkv*d < 2^33 (append, gather); total*Hq < 2^31.  Any Hq that Hkv
+ * divides.  Row strides (elements) are multiples of 8 and at least a row
+ * long: k, v and q may be parts of one projection's output.  All base
+ * pointers are 16-byte aligned but for int32 arrays and lse (4).  total = 0
+ * is a step without rows: MSA_OK, nothing enqueued.
+ *
+ * msa_cache_workspace_size: bytes of workspace for all calls of this section
+ * (0 for arguments that they reject).  256-byte aligned, status word first,
+ * as msa_workspace_size describes; append and gather use the status word only.
+ */
+MSA_API size_t msa_cache_workspace_size(int Hq, int Hkv, int d);
+
+/*
+ * The step's new rows k, v ([total] rows of Hkv*d bf16 values every k_stride /
+ * v_stride elements) into the pages of their positions, and, unless k_idx and
+ * k_idx_pages are both NULL, the index keys k_idx ([total] rows of d_idx bf16
+ * values) into k_idx_pages [num_pages][block][d_idx].  Rows of the stores that
+ * no new row maps to are left as they were.  Two rows of one call must not
+ * map to the same place.
+ */
+MSA_API msa_status msa_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                 const void *k_idx, int64_t k_idx_stride, void *k_pages,
+                                 void *v_pages, void *k_idx_pages, const int32_t *page_table,
+                                 int page_stride, int num_pages, const int32_t *cu,
+                                 const int32_t *kv_len, int Bt, int total, int Hkv, int d,
+                                 int d_idx, int block, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+MSA_API msa_status msa_kv_append_i8(const void *k, int64_t k_stride, const void *v,
+                                    int64_t v_stride, const void *k_idx, int64_t k_idx_stride,
+                                    int8_t *k_pages, int8_t *v_pages, float *k_scales,
+                                    float *v_scales, void *k_idx_pages, const int32_t *page_table,
+                                    int page_stride, int num_pages, const int32_t *cu,
+                                    const int32_t *kv_len, int Bt, int total, int Hkv, int d,
+                                    int d_idx, int block, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/*
+ * The cached rows of the step's positions as packed bf16 k, v [total][Hkv][d]
+ * (n_b = kv_len[b] reads whole contexts back, e.g. for the contiguous prefill
+ * calls).  int8: code * scale in fp32, rounded once.  Rows whose position is
+ * negative or whose page does not exist are zeros.
+ */
+MSA_API msa_status msa_kv_gather(const void *k_pages, const void *v_pages,
+                                 const int32_t *page_table, int page_stride, int num_pages,
+                                 const int32_t *cu, const int32_t *kv_len, void *k, void *v,
+                                 int Bt, int total, int Hkv, int d, int block, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+MSA_API msa_status msa_kv_gather_i8(const int8_t *k_pages, const int8_t *v_pages,
+                                    const float *k_scales, const float *v_scales,
+                                    const int32_t *page_table, int page_stride, int num_pages,
+                                    const int32_t *cu, const int32_t *kv_len, void *k, void *v,
+                                    int Bt, int total, int Hkv, int d, int block, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/*
+ * Attention of the step's rows over their cached contexts (append first: the
+ * step's own tokens are read from the pages).  q: [total] rows of Hq*d bf16
+ * values every q_stride elements.  A query at position t sees the keys
+ *     j <= t  with  window == 0  or  j > t - window  or  j < sinks
+ * (window > 0: the last `window` keys, itself among them, and the first
+ * `sinks` ones; sinks is ignored without a window).  Scale 1/sqrt(d).
+ * out [total][Hq][d] bf16 (fp32 sums, rounded once), lse [total][Hq] fp32
+ * (natural log); a row that sees no key gets out 0 and lse -inf.
+ * max_q: the largest n_b of the step, or 0 if the caller does not know it; it
+ * chooses between kernels and changes no result beyond rounding.
+ * Cache rows at or past kv_len[b], and rows that no row of the step sees, do
+ * not matter, whatever they hold.  A key that one row of the step sees and
+ * another does not must have finite values in v_pages (bf16).
+ */
+MSA_API msa_status msa_attn_paged(const void *q, int64_t q_stride, const void *k_pages,
+                                  const void *v_pages, const int32_t *page_table, int page_stride,
+                                  int num_pages, const int32_t *cu, const int32_t *kv_len,
+                                  void *out, float *lse, int Bt, int total, int max_q, int Hq,
+                                  int Hkv, int d, int block, int window, int sinks,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+MSA_API msa_status msa_attn_paged_i8(const void *q, int64_t q_stride, const int8_t *k_pages,
+                                     const int8_t *v_pages, const float *k_scales,
+                                     const float *v_scales, const int32_t *page_table,
+                                     int page_stride, int num_pages, const int32_t *cu,
+                                     const int32_t *kv_len, void *out, float *lse, int Bt,
+                                     int total, int max_q, int Hq, int Hkv, int d, int block,
+                                     int window, int sinks, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/*
+ * The sparse branch of a decode step on int8 pages: msa_sparse_attn_paged
+ * (same ids, same keys) with the 8-bit stores and the output types of this
+ * section: out [Bt][1][Hq][d] bf16, lse [Bt][1][Hq] fp32.  K <= 32.
+ */
+MSA_API msa_status msa_sparse_attn_paged_i8(const void *q, const int8_t *k_pages,
+                                            const int8_t *v_pages, const float *k_scales,
+                                            const float *v_scales, const int32_t *page_table,
+                                            int page_stride, int num_pages, const int32_t *ids,
+                                            void *out, float *lse, int Bt, int T, int Hq, int Hkv,
+                                            int d, int block, int K, void *workspace,
+                                            size_t workspace_bytes, void *stream);
+
+/*
  * Instrumented variants (profiling): the same work as msa_index_topk and
  * msa_sparse_attn, with optional CUDA events recorded on `stream`
  * immediately before (start[i]) and after (stop[i]) the kernels of stage i.
