@@ -57,16 +57,19 @@ struct PagedAttn {
     float scale_log2 = 0.f;          // log2(e) / sqrt(d)
     float *part_o = nullptr;         // split pieces, fp32 [pieces][rows][d]
     float *part_lse = nullptr;       // their log2-domain lse [pieces][rows]
+    int *counters = nullptr;         // finished pieces per run: zero between calls
     int *status = nullptr;
 };
 
-constexpr int kSplitTileRows = 16;   // query rows per tile of the split kernel (one MMA M)
-constexpr int kSplitKeys = 64;       // keys per tile of the split kernel
-constexpr int kSplitMaxCtas = 1024;  // CTAs of the split kernel (workspace bound)
+constexpr int kSplitKeys = 128;      // keys per tile of the split kernel
+constexpr int kSplitMaxRows = 32;    // query rows per tile, at most
+constexpr int kSplitMaxCtas = kWsCounters;  // CTAs of the split kernel (workspace bound)
 
 // Rows of the K / V tensor map boxes of the split kernel.
 inline int split_box_rows(int block) { return block < kSplitKeys ? block : kSplitKeys; }
-cudaError_t launch_split_attn(const PagedAttn &a, const CUtensorMap &tk, const CUtensorMap &tv,
-                              int num_sms, cudaStream_t st);
+// rows: query rows that a (sequence, kv head) pair has, as far as the caller
+// knows; it chooses the tile height.
+cudaError_t launch_split_attn(const PagedAttn &a, int rows, const CUtensorMap &tk,
+                              const CUtensorMap &tv, int num_sms, cudaStream_t st);
 
 }  // namespace msa

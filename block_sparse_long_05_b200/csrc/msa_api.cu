@@ -69,7 +69,7 @@ int kv_group_within(const Shape &sh, size_t budget) {
 // kv_group: prefill kv heads per attention launch (0: all of them).
 WsLayout layout_for(const Shape &sh, bool with_attn, int kv_group = 0) {
     WsLayout L;
-    size_t off = 256;  // status word + padding
+    size_t off = kWsHeader;  // status word, counters
     auto take = [&](size_t bytes) {
         const size_t o = off;
         off = align_up(off + bytes, 256);

@@ -18,15 +18,16 @@ using namespace msa;
 namespace {
 
 constexpr size_t kStatusBytes = 256;
+static_assert(kWsHeader == MSA_WORKSPACE_HEADER_BYTES, "header documented in msa.h");
 
 struct CacheWs {
     size_t part_o, part_lse, total;
 };
 
 CacheWs cache_layout(int d) {
-    const size_t rows = static_cast<size_t>(2) * kSplitMaxCtas * kSplitTileRows;
+    const size_t rows = static_cast<size_t>(2) * kSplitMaxCtas * kSplitMaxRows;
     CacheWs w;
-    w.part_o = kStatusBytes;
+    w.part_o = kWsHeader;
     w.part_lse = align_up(w.part_o + rows * d * 4, 256);
     w.total = align_up(w.part_lse + rows * 4, 256);
     return w;
@@ -158,23 +159,26 @@ bool store_map(CUtensorMap *m, const void *pages, int num_pages, int block, int 
 
 // Shared by the dense and the sparse entry: `a` has everything but the
 // workspace regions and the scale of the scores.
-msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int num_pages, void *ws,
-                  void *stream) {
+// max_q: rows of the longest sequence, as far as the caller knows.
+msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int num_pages, int max_q,
+                  void *ws, void *stream) {
     const CacheWs L = cache_layout(a.c.d);
     unsigned char *base = static_cast<unsigned char *>(ws);
     a.part_o = reinterpret_cast<float *>(base + L.part_o);
     a.part_lse = reinterpret_cast<float *>(base + L.part_lse);
+    a.counters = reinterpret_cast<int *>(base + kStatusBytes);
     a.status = static_cast<int *>(ws);
     a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(a.c.d));
     const int sms = num_sms_current();
     if (sms <= 0) return MSA_ERR_CUDA;
     const bool i8 = a.c.k_scales != nullptr;
-    const int rows = split_box_rows(a.step.block);
+    const int box = split_box_rows(a.step.block);
     CUtensorMap tk, tv;
-    if (!store_map(&tk, k_pages, num_pages, a.step.block, a.c.Hkv, a.c.d, rows, i8) ||
-        !store_map(&tv, v_pages, num_pages, a.step.block, a.c.Hkv, a.c.d, rows, i8))
+    if (!store_map(&tk, k_pages, num_pages, a.step.block, a.c.Hkv, a.c.d, box, i8) ||
+        !store_map(&tv, v_pages, num_pages, a.step.block, a.c.Hkv, a.c.d, box, i8))
         return MSA_ERR_CUDA;
-    const cudaError_t e = launch_split_attn(a, tk, tv, sms, static_cast<cudaStream_t>(stream));
+    const int rows = max_q < kSplitMaxRows ? max_q * a.G : kSplitMaxRows + 1;
+    const cudaError_t e = launch_split_attn(a, rows, tk, tv, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
 
@@ -211,7 +215,7 @@ msa_status attn_impl(const void *q, int64_t q_stride, const void *k_pages, const
     // positions stay below 2^30, so a longer window hides nothing
     a.window = window < (1 << 30) ? window : 1 << 30;
     a.sinks = window ? sinks : 0;
-    return attend(a, k_pages, v_pages, num_pages, ws, stream);
+    return attend(a, k_pages, v_pages, num_pages, max_q > 0 && max_q < total ? max_q : total, ws, stream);
 }
 
 }  // namespace
@@ -324,7 +328,7 @@ msa_status msa_sparse_attn_paged_i8(const void *q, const int8_t *k_pages, const 
     a.ids = ids;
     a.K = K;
     a.T = T;
-    return attend(a, k_pages, v_pages, num_pages, workspace, stream);
+    return attend(a, k_pages, v_pages, num_pages, 1, workspace, stream);
 }
 
 }  // extern "C"

@@ -56,6 +56,11 @@ struct OwnWork {
     int *counters;   // per attention launch: (items, cursor)
 };
 
+// Every workspace begins with a header that holds state between calls: the
+// status word (256 bytes), then counters that each call leaves at zero.
+constexpr int kWsCounters = 512;
+constexpr size_t kWsHeader = 256 + static_cast<size_t>(kWsCounters) * 4;
+
 // Workspace layout.  Offsets are in bytes from the workspace base; every
 // region is 256-byte aligned.  Status word at offset 0.
 struct WsLayout {

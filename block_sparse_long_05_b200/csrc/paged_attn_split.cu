@@ -2,29 +2,43 @@
 // (single tokens, short chunks, and the sparse branch on int8 pages).
 //
 // With the rows of one (sequence, kv head) numbered r = i * G + g (token i,
-// head g of the group), a tile of 16 rows attends its keys j with
+// head g of the group), a tile of R = 8, 16 or 32 rows attends its keys j with
 //     s_j = (q . k_j) / sqrt(d),  m = max s_j,  l = sum exp(s_j - m),
 //     o = sum exp(s_j - m) v_j / l,  lse = m + ln l,
-// in one pass over the keys with a running m and l.  With int8 pages k_j =
-// code_j * sk_j and v_j = code_j * sv_j: the codes enter the matrix products
-// exactly (a signed byte fits bf16), sk_j scales the scores and sv_j the
-// weights, both in fp32, so no dequantised value is rounded.
+// in one pass over the keys, 128 at a time, with a running m and l.
 //
-// Few rows read many keys once, so HBM bounds it: 16 rows x 64 keys need
-// 48 mma per warp for 8 KB (bf16) or 4 KB (int8) of K and V.  Therefore
-//  - the key tiles of all (sequence, row tile, kv head) segments form one
-//    list that is cut into equal runs, one per CTA, two CTAs per SM: a batch
-//    with contexts of any lengths keeps every SM streaming to the end;
-//  - a producer warp keeps a ring of about 100 KB per CTA filled by TMA,
-//    across segment borders, and looks the pages up 32 tiles at a time;
-//  - four warps take 16 keys of a 64-key tile each, with their own m, l and
-//    o in registers, and meet only at the end of a segment;
-//  - a segment that lies in several runs leaves one fp32 piece per run, which
-//    the combine kernel (programmatic dependent launch) merges in run order:
-//    no atomics, the same result every time.
-// The weights enter the second product as two bf16 terms (hi + lo, 16 bits
-// of mantissa): the matrix unit is idle most of the time here, and the
-// output then carries its own final rounding only.
+// Few rows read many keys once, so HBM bounds it, and the instructions spent
+// per key come next.  Both products therefore run on the tensor core with the
+// keys (then the value columns) as its 128 rows and the query rows as its
+// columns, and take K and V as TMA left them in shared memory:
+//     S^T [128 keys][rows] = K Q^T,   O^T [d][rows] = V^T P^T.
+// A thread then holds one key's scores of all rows, and afterwards one value
+// column's sums of all rows, in its own registers.
+//
+// int8 pages (k_j = code * sk_j, v_j = code * sv_j) are never converted: the
+// products are integer ones (exact), of Q and P written in 7-bit digits,
+//     q = 2^e (x2 2^14 + x1 2^7 + x0),  |x| <= 64,  e from the row's largest |q|
+//     p_j sv_j / svmax = 2^-27 (y3 2^21 + y2 2^14 + y1 2^7 + y0),  0 <= y < 128
+// each digit a column of its own.  q keeps 20 bits below its row's largest
+// value (a bf16 has 8 of its own); p keeps 27 bits below the row's largest so
+// far, because the many small weights beside a large one (a first token that
+// draws most of the weight) may make up the output: with 20 bits their
+// rounding would show.  sk, sv and the digits' weights are applied in fp32.  (A kernel that turned
+// the codes into bf16 fragments for mma.sync spent 700 instructions per warp
+// on 16 keys and reached 2.6 TB/s; this one spends about 300 on 32.)
+// bf16 pages take Q as it is and P as two bf16 terms (hi + lo, 16 bits).
+//
+//  - The key tiles of all (sequence, row tile, kv head) segments form one
+//    list that is cut into equal runs, one per CTA: a batch with contexts of
+//    any lengths keeps every SM streaming to the end.
+//  - A producer warp keeps a ring of about 100 KB (200 KB with one CTA per
+//    SM) filled by TMA, across segment borders, and looks the pages up 32
+//    tiles at a time.
+//  - A segment that lies in several runs leaves one fp32 piece per run, and the
+//    CTA that finishes the last piece merges them in run order.  An atomic
+//    counter tells it that it is the last; which CTA that is has no influence
+//    on the result.  (A second kernel for the merge cost 4 us of device time
+//    and 3 us of launch on a call of 8 us.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,10 +52,10 @@ namespace msa {
 
 namespace {
 
-constexpr int kComputeWarps = 4;
-constexpr int kSplitThreads = 32 * (kComputeWarps + 1);
-constexpr int kTileRows = kSplitTileRows, kKeys = kSplitKeys;
-constexpr int kMinRun = 2;  // tiles per run: below it a combine costs more than the run saves
+constexpr int kKeys = 128;                   // keys per tile: M of the first product
+constexpr int kThreads = 128 + 32;           // warps 0-3: one key (then one value column) per
+                                             // thread; warp 4: producer
+constexpr int kMinRun = 2;  // tiles per run: below it the merge costs more than the run saves
 constexpr float kLn2f = 0.6931471805599453f;
 
 // ------------------------------------------------------------ the work list
@@ -55,7 +69,7 @@ struct Seq {
     int nk;       // key tiles per row tile (upper bound over the row tiles)
 };
 
-__device__ __forceinline__ Seq seq_of(const PagedAttn &a, int b) {
+__device__ __forceinline__ Seq seq_of(const PagedAttn &a, int b, int R) {
     Seq s;
     if (a.ids) {  // sparse branch: the tiles of K selected blocks, one row per sequence
         s.cu0 = b;
@@ -73,13 +87,13 @@ __device__ __forceinline__ Seq seq_of(const PagedAttn &a, int b) {
         s.off = len - s.n;
         s.nk = (kv + kKeys - 1) / kKeys;
         if (a.window) {
-            const int span = min(s.n, kTileRows / a.G + 2);  // tokens of a row tile
+            const int span = min(s.n, R / a.G + 2);  // tokens of a row tile
             const int near = (a.window + span) / kKeys + 3;
             s.nk = min(s.nk, near + (min(a.sinks, kv) + kKeys - 1) / kKeys);
         }
         s.nk = max(s.nk, 1);  // rows without a key are written too
     }
-    s.nt = (s.n * a.G + kTileRows - 1) / kTileRows;
+    s.nt = (s.n * a.G + R - 1) / R;
     return s;
 }
 
@@ -96,12 +110,12 @@ struct RowTile {
     int na, skip, count;
 };
 
-__device__ __forceinline__ RowTile row_tile(const PagedAttn &a, const Seq &s, int rt) {
+__device__ __forceinline__ RowTile row_tile(const PagedAttn &a, const Seq &s, int rt, int R) {
     RowTile t;
     t.rows = s.n * a.G;
-    t.r0 = rt * kTileRows;
+    t.r0 = rt * R;
     t.tmin = s.off + t.r0 / a.G;
-    t.tmax = s.off + (min(t.r0 + kTileRows, t.rows) - 1) / a.G;
+    t.tmax = s.off + (min(t.r0 + R, t.rows) - 1) / a.G;
     t.na = t.skip = 0;
     if (a.ids) {
         t.count = s.nk;
@@ -118,68 +132,77 @@ __device__ __forceinline__ RowTile row_tile(const PagedAttn &a, const Seq &s, in
     return t;
 }
 
-// Exclusive prefix of the work over the sequences: total, and the sequence
-// and offset that hold unit u.  All threads of the CTA; blockDim <= 256.
+// Where a run begins: sequence and offset in it.  All threads of the CTA take
+// part; blockDim is a multiple of 32 and at most 256.
 struct Found {
     int b;
     long long off;
+    long long work;   // tiles of the step
+    long long start;  // first tile of this CTA's run
+    long long run;    // tiles per run
 };
-__device__ long long total_work(const PagedAttn &a, long long *sm) {
-    long long w = 0;
-    for (int b = threadIdx.x; b < a.step.Bt; b += blockDim.x) {
-        const Seq s = seq_of(a, b);
-        w += seq_work(a, s);
+
+__device__ __forceinline__ long long run_length(long long work, int ctas) {
+    const long long per = (work + ctas - 1) / ctas;
+    return per > kMinRun ? per : kMinRun;
+}
+
+// sm: [0..7] warp sums, [8] sequence, [9] offset
+__device__ __forceinline__ Found find_run(const PagedAttn &a, int R, long long *sm) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int Bt = a.step.Bt, chunks = (Bt + blockDim.x - 1) / blockDim.x;
+    auto work_of = [&](int b) -> long long {
+        if (b >= Bt) return 0;
+        const Seq s = seq_of(a, b, R);
         // a context longer than its page-table row: the keys past it do not exist
         if (s.off + s.n > s.cap) atomicOr(a.status, kDevBadIds);
-    }
+        return seq_work(a, s);
+    };
+    Found f;
+    f.b = 0;
+    f.off = f.work = 0;
+    // one chunk of sequences (the usual case): its work stays in a register;
+    // otherwise a first sweep adds up and a second one searches
+    long long w = work_of(threadIdx.x);
+    for (int c = 1; c < chunks; ++c) w += work_of(c * blockDim.x + threadIdx.x);
+    const long long mine = w;
 #pragma unroll
     for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = w;
+    if (lane == 0) sm[warp] = w;
     __syncthreads();
-    long long sum = 0;
-    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) sum += sm[i];
-    __syncthreads();
-    return sum;
-}
-__device__ Found find_unit(const PagedAttn &a, long long u, long long *sm) {
-    // sm: [0..7] warp sums, [8] sequence, [9] offset
+    for (int i = 0; i < nw; ++i) f.work += sm[i];
+    f.run = run_length(f.work, gridDim.x);
+    f.start = f.run * blockIdx.x;
+    if (f.start >= f.work) return f;
     long long base = 0;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    for (int b0 = 0; b0 < a.step.Bt; b0 += blockDim.x) {
-        const int b = b0 + threadIdx.x;
-        const long long w = b < a.step.Bt ? seq_work(a, seq_of(a, b)) : 0;
-        long long p = w;
+    for (int c = 0; c < chunks; ++c) {
+        const long long x = chunks == 1 ? mine : work_of(c * blockDim.x + threadIdx.x);
+        long long p = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xFFFFFFFFu, p, o);
             if (lane >= o) p += y;
         }
+        __syncthreads();
         if (lane == 31) sm[warp] = p;
         __syncthreads();
-        long long before = base, chunk = 0;
+        long long before = base, all = 0;
         for (int i = 0; i < nw; ++i) {
             if (i < warp) before += sm[i];
-            chunk += sm[i];
+            all += sm[i];
         }
-        const long long first = before + p - w;
-        if (u >= first && u < first + w) {
-            sm[8] = b;
-            sm[9] = u - first;
+        const long long first = before + p - x;
+        if (f.start >= first && f.start < first + x) {
+            sm[8] = c * static_cast<int>(blockDim.x) + threadIdx.x;
+            sm[9] = f.start - first;
         }
-        base += chunk;
-        __syncthreads();
-        if (u < base) break;
+        base += all;
+        if (f.start < base) break;
     }
-    Found f;
+    __syncthreads();
     f.b = static_cast<int>(sm[8]);
     f.off = sm[9];
-    __syncthreads();
     return f;
-}
-
-__device__ __forceinline__ long long run_length(long long work, int ctas) {
-    const long long per = (work + ctas - 1) / ctas;
-    return per > kMinRun ? per : kMinRun;
 }
 
 // A run's segments in order: sequence, row tile, kv head, key tiles [x0, x1).
@@ -187,15 +210,15 @@ struct Walk {
     Seq s;
     int b, rt, h, x0, x1;
     long long pos, end, off;
-    __device__ __forceinline__ Walk(const Found &f, long long start, long long stop)
-        : b(f.b), pos(start), end(stop), off(f.off) {}
-    __device__ __forceinline__ bool next(const PagedAttn &a) {
+    __device__ __forceinline__ explicit Walk(const Found &f)
+        : b(f.b), pos(f.start), end(min(f.start + f.run, f.work)), off(f.off) {}
+    __device__ __forceinline__ bool next(const PagedAttn &a, int R) {
         if (pos >= end) return false;
-        s = seq_of(a, b);
+        s = seq_of(a, b, R);
         while (off >= seq_work(a, s)) {  // (only after a step; bounded by Bt)
             off = 0;
             if (++b >= a.step.Bt) return false;
-            s = seq_of(a, b);
+            s = seq_of(a, b, R);
         }
         const long long seg = off / s.nk;
         x0 = static_cast<int>(off - seg * s.nk);
@@ -210,30 +233,39 @@ struct Walk {
 };
 
 // ------------------------------------------------------------ tile geometry
-template <int D, bool I8>
+constexpr int round_up(int x, int m) { return (x + m - 1) / m * m; }
+
+template <int D, bool I8, int R>
 struct Tile {
-    static constexpr int ROWB = D * (I8 ? 1 : 2) < 128 ? D * (I8 ? 1 : 2) : 128;  // smem row
-    static constexpr int REGS = D * (I8 ? 1 : 2) / ROWB;  // 128-byte wide regions
+    static constexpr int EB = I8 ? 1 : 2;
+    static constexpr int ROWB = D * EB < 128 ? D * EB : 128;  // bytes of a shared-memory row
+    static constexpr int REGS = D * EB / ROWB;                // 128-byte wide regions
     static constexpr int REGION = kKeys * ROWB;
-    static constexpr int BYTES = REGS * REGION;           // K or V of 64 keys
-    static constexpr int STAGE = 2 * BYTES;
-    static constexpr int STAGES = STAGE >= 32768 ? 3 : STAGE >= 16384 ? 6 : 8;
-    static constexpr int CW = I8 ? D / 8 : 8;  // columns of V per thread group and region
-    static constexpr int NT = D / 8;           // 8-column tiles of O
-    static constexpr int KST = D / 16;         // k-steps of q . k
+    static constexpr int BYTES = REGS * REGION;               // K or V of a tile
+    static constexpr int STAGE = 2 * BYTES;                   // V, then K
+    static constexpr int CTAS = STAGE > 32768 ? 1 : 2;        // per SM
+    // columns of the products (a multiple of 16 each): scores, outputs
+    static constexpr int NS = I8 ? round_up(3 * R, 16) : round_up(R, 16);
+    static constexpr int NO = I8 ? 4 * R : 2 * R;
+    static constexpr int QBYTES = NS * D * EB;
+    static constexpr int PBYTES = NO * kKeys * EB;
+    // the ring takes what the 227 KB of an SM leave
+    static constexpr int STAGES = STAGE > 32768 ? 3 : STAGE > 16384 ? (R <= 8 || (!I8 && R <= 16) ? 3 : 2) : (R <= 8 ? 6 : 5);
+    static constexpr int TMEM = NS + NO <= 32 ? 32 : NS + NO <= 64 ? 64 : NS + NO <= 128 ? 128 : 256;
 };
 
-struct alignas(8) StageMeta {
-    int pos[2];  // first key of each 32-key half; -1: nothing there
+struct alignas(16) StageMeta {
+    int pos[4];  // first key of each 32-key quarter; -1: nothing there
 };
 
-constexpr int kMergeBytes = kComputeWarps * kTileRows * 32 * 4;
+constexpr int kScaleBytes = 2 * kKeys * 4;  // K and V scales of a stage
+constexpr int kMergeFloats = 1024;          // weights of a chunk of pieces (in the buffer of P)
 
-template <int D, bool I8>
+template <int D, bool I8, int R>
 constexpr size_t split_smem_bytes() {
-    using T = Tile<D, I8>;
-    return 1024 + static_cast<size_t>(T::STAGES) * (T::STAGE + sizeof(StageMeta) + 16 + (I8 ? 512 : 0)) +
-           kMergeBytes + kComputeWarps * kTileRows * 8 + 256;
+    using T = Tile<D, I8, R>;
+    return 1024 + static_cast<size_t>(T::STAGES) * T::STAGE + round_up(T::QBYTES, 1024) +
+           round_up(T::PBYTES, 1024) + (I8 ? T::STAGES * kScaleBytes : 0) + (R + 1) * 16 + R * 20 + 16 + T::STAGES * (sizeof(StageMeta) + 16) + 128;
 }
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -244,100 +276,215 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         : "memory");
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// Maximum over the warp (a NaN counts as absent).
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
+// 8 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
 }
 
-// Two signed bytes (in the low bytes of the 16-bit halves of x) as bf16, both
-// exact: 128 + (low 7 bits) minus 128, or minus 256 where the sign bit is
-// set.  0x4300 is 128 in bf16, its last mantissa bit counts 1, and the sign
-// bit of the byte falls on the lowest exponent bit (0x4380 is 256).
-__device__ __forceinline__ uint32_t s8x2_bf16(uint32_t x) {
-    const uint32_t hi = (x & 0x007F007Fu) | 0x43004300u, lo = (x & 0x00800080u) | 0x43004300u;
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&hi),
-                                     *reinterpret_cast<const __nv_bfloat162 *>(&lo));
-    return *reinterpret_cast<const uint32_t *>(&r);
+// x2 2^14 + x1 2^7 + x0 of signed sums (x0, x1 below 2^21).
+__device__ __forceinline__ float from_digits(uint32_t x0, uint32_t x1, uint32_t x2) {
+    const int lo = static_cast<int>(x1) * 128 + static_cast<int>(x0);
+    return fmaf(static_cast<float>(static_cast<int>(x2)), 16384.f, static_cast<float>(lo));
 }
 
-// Offset of 16-byte piece c of row r of a tile region.
+// Byte offset of 16-byte piece c of row r of a swizzled region.
 template <int ROWB>
 __device__ __forceinline__ uint32_t piece_at(uint32_t r, uint32_t c) {
     if (ROWB == 128) return sw128_offset(r, c);
-    return r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);  // 64-byte swizzle
+    return r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
+}
+
+// Operand descriptors.  Key-major rows (K, Q, P): the contraction runs along a
+// row; V^T: it runs over the rows, and a row holds 64 bf16 or D codes of d.
+// With d = 64 the second half of V^T's 128 rows is whatever lies one region
+// further (the K tile); its sums are never read.
+template <int ROWB>
+__device__ __forceinline__ uint64_t row_desc(uint32_t addr) {
+    return ROWB == 128 ? sdesc_sw128(addr, 16, 1024) : sdesc_sw64(addr);
+}
+template <int ROWB, int REGION>
+__device__ __forceinline__ uint64_t col_desc(uint32_t addr) {
+    if (ROWB == 128) return sdesc_sw128(addr, REGION, 1024);
+    return (sdesc_sw64(addr) & ~(0x3FFFull << 16)) | (static_cast<uint64_t>(REGION >> 4) << 16);
+}
+
+constexpr uint32_t kIdescAMn = 1u << 15;  // A runs along M in memory
+
+// ===========================================================================
+// Merge of the pieces of a segment whose first run is c0 and last run c1:
+//   lse = log2 sum 2^lse_p,  out = sum 2^(lse_p - lse) o_p
+// by the 128 threads of warps 0-3, a value column each.  wt: kMergeFloats.
+// ===========================================================================
+template <int D, int R>
+__device__ __noinline__ void merge_pieces(const PagedAttn &a, const RowTile &t, int cu0, int h, int c0,
+                                          int c1, bool first, float *wt) {
+    constexpr int RG = 8;                      // rows at a time
+    constexpr int CH = kMergeFloats / RG - 1;  // pieces per chunk; the last row holds the maxima
+    const int tid = threadIdx.x, pieces = c1 - c0 + 1, col = tid < D ? tid : 0;
+    // the first run's piece is its last one, unless the run begins with it
+    auto slot = [&](int p) { return 2ll * (c0 + p) + (p == 0 && !first ? 1 : 0); };
+#pragma unroll 1
+    for (int rg = 0; rg < min(t.rows - t.r0, R); rg += RG) {
+        const int live = min(t.rows - t.r0, R) - rg;
+        float acc[RG], sum[RG], top[RG];
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+            acc[r] = sum[r] = 0.f;
+            top[r] = -INFINITY;
+        }
+#pragma unroll 1
+        for (int p0 = 0; p0 < pieces; p0 += CH) {
+            const int m = min(CH, pieces - p0);
+            named_barrier(1, 128);
+            for (int e = tid; e < m * RG; e += 128)
+                wt[e] = e % RG < live ? __ldcg(a.part_lse + slot(p0 + e / RG) * R + rg + e % RG) : -INFINITY;
+            named_barrier(1, 128);
+            if (tid < RG) {
+                float g = -INFINITY;
+                for (int p = 0; p < m; ++p) g = fmaxf(g, wt[p * RG + tid]);
+                wt[CH * RG + tid] = g;
+            }
+            named_barrier(1, 128);
+            float f[RG];
+#pragma unroll
+            for (int r = 0; r < RG; ++r) {
+                const float g = fmaxf(top[r], wt[CH * RG + r]);
+                f[r] = top[r] == -INFINITY ? 0.f : ex2_approx(top[r] - g);
+                top[r] = g;
+            }
+            for (int e = tid; e < m * RG; e += 128) {
+                const float l = wt[e], g = fmaxf(wt[CH * RG + e % RG], -3e38f);
+                // relative to this chunk's maximum; 0: the piece has no key of the row
+                // (a weight that underflows stays above 0, for the sake of a NaN)
+                const float w = ex2_approx(l - g);
+                wt[e] = l == -INFINITY ? 0.f : w == 0.f ? 1.2e-38f : w;
+            }
+            named_barrier(1, 128);
+#pragma unroll
+            for (int r = 0; r < RG; ++r) {
+                acc[r] *= f[r];
+                sum[r] *= f[r];
+            }
+            float part[RG], psum[RG];
+#pragma unroll
+            for (int r = 0; r < RG; ++r) part[r] = psum[r] = 0.f;
+#pragma unroll 1
+            for (int p = 0; p < m; p += 4) {
+                float y[4][RG];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int r = 0; r < RG; ++r)
+                        y[k][r] = p + k < m && r < live ? __ldcg(a.part_o + (slot(p0 + p + k) * R + rg + r) * D + col) : 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (p + k >= m) break;
+#pragma unroll
+                    for (int r = 0; r < RG; ++r) {
+                        const float w = wt[(p + k) * RG + r];
+                        psum[r] += w;
+                        part[r] += w == 0.f ? 0.f : w * y[k][r];
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RG; ++r) {
+                const float g = wt[CH * RG + r];
+                const float w = g == -INFINITY ? (psum[r] == psum[r] ? 0.f : 1.f) : ex2_approx(g - top[r]);
+                acc[r] += w * part[r];
+                sum[r] += w * psum[r];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+            if (r >= live || tid >= D) continue;
+            const int row = t.r0 + rg + r, tok = row / a.G;
+            const long long orow = (static_cast<long long>(cu0) + tok) * a.Hq + static_cast<long long>(h) * a.G + (row - tok * a.G);
+            const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
+            static_cast<__nv_bfloat16 *>(a.out)[orow * D + tid] = __float2bfloat16_rn(acc[r] * inv);
+            if (tid == 0) a.lse[orow] = sum[r] == 0.f ? -INFINITY : (top[r] + __log2f(sum[r])) * kLn2f;
+        }
+        named_barrier(1, 128);
+    }
 }
 
 // ===========================================================================
-// One run per CTA.  Warp 4: producer; warps 0-3: 16 keys of each tile.
-// In an mma fragment a thread (gq = lane / 4, c = lane % 4) holds rows gq and
-// gq + 8.  The order of the d values over the k-steps, and of the columns of
-// V over the 8-column tiles, is chosen so that a thread reads K and V in
-// 16-byte pieces without bank conflicts: K pieces 2c and 2c + 1 of its key
-// (Q is loaded in the same order), V pieces gq of its four keys, whose values
-// are paired key by key by byte permutes.
+// One run per CTA.
 // ===========================================================================
-template <int D, bool I8>
-__global__ void __launch_bounds__(kSplitThreads, 2) split_attn_kernel(
+template <int D, bool I8, int R>
+__global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __grid_constant__ PagedAttn a) {
-    using T = Tile<D, I8>;
+    using T = Tile<D, I8, R>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *ring = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    float *merge = reinterpret_cast<float *>(ring + T::STAGES * T::STAGE);  // [warp][row][32]
-    float2 *ml = reinterpret_cast<float2 *>(merge + kMergeBytes / 4);       // [warp][row] (m, l)
-    float *scales = reinterpret_cast<float *>(ml + kComputeWarps * kTileRows);  // [stage][2][64]
-    uint64_t *full = reinterpret_cast<uint64_t *>(scales + (I8 ? T::STAGES * 128 : 0));
+    unsigned char *q_s = ring + T::STAGES * T::STAGE;
+    unsigned char *p_s = q_s + round_up(T::QBYTES, 1024);
+    float *scales = reinterpret_cast<float *>(p_s + round_up(T::PBYTES, 1024));  // [stage][K, V][128]
+    static_assert(T::PBYTES >= kMergeFloats * 4, "merge weights");
+    float4 *tops = reinterpret_cast<float4 *>(scales + (I8 ? T::STAGES * 2 * kKeys : 0));  // [row] maxima of the 4 warps; [R]: of sv
+    float *qscale = reinterpret_cast<float *>(tops + R + 1);       // [R] factor of a row's scores
+    float *maxima = qscale + R;                                    // [2][R] the rows' m, tile about
+    int *rowpos = reinterpret_cast<int *>(maxima + 2 * R);         // [R] position, -1: no such row
+    int *poison = rowpos + R;                                      // [R] a seen key's sv is not finite
+    StageMeta *meta = reinterpret_cast<StageMeta *>(
+        (reinterpret_cast<uintptr_t>(poison + R) + 15) & ~static_cast<uintptr_t>(15));
+    uint64_t *full = reinterpret_cast<uint64_t *>(meta + T::STAGES);
     uint64_t *empty = full + T::STAGES;
-    StageMeta *meta = reinterpret_cast<StageMeta *>(empty + T::STAGES);
-    long long *scan = reinterpret_cast<long long *>(meta + T::STAGES);  // [10]
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(scan + 10);
+    uint64_t *bar_s = empty + T::STAGES, *bar_o = bar_s + 1;
+    long long *scan = reinterpret_cast<long long *>(bar_o + 1);  // [10]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(scan + 10);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *last_piece = abort_flag + 1;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < T::STAGES; ++i) {
             mbar_init(full + i, 1);
-            mbar_init(empty + i, kComputeWarps);
+            mbar_init(empty + i, 1);
         }
+        mbar_init(bar_s, 1);
+        mbar_init(bar_o, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    const long long work = total_work(a, scan);
-    const long long run = run_length(work, gridDim.x);
-    const long long start = run * blockIdx.x, stop = min(start + run, work);
-    if (start >= stop) return;
-    Walk walk(find_unit(a, start, scan), start, stop);
+    const Found found = find_run(a, R, scan);
+    if (found.start >= found.work) return;
+    Walk walk(found);
     const int block = a.step.block;
 
-    if (warp == kComputeWarps) {
+    if (warp == 4) {
         // -------------------------------------------------------- producer
         uint32_t it = 0;
-        const int half = min(block, kKeys);  // keys per TMA box
+        const int box = min(block, kKeys);  // keys per TMA box
         bool ok = true;
-        while (ok && walk.next(a)) {
-            const RowTile t = row_tile(a, walk.s, walk.rt);
+        while (ok && walk.next(a, R)) {
+            const RowTile t = row_tile(a, walk.s, walk.rt, R);
             const int x1 = min(walk.x1, t.count);
             for (int xb = walk.x0; xb < x1 && ok; xb += 32) {
-                // page and position of this lane's tile (two boxes with 32-key blocks)
-                int pos[2] = {-1, -1}, z[2] = {0, 0};
+                // positions and store rows of this lane's tile, by 32-key quarters
+                int pos[4] = {-1, -1, -1, -1}, z[4] = {0, 0, 0, 0};
                 const int x = xb + lane;
                 if (x < x1) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (i == 1 && block >= kKeys) {
-                            pos[1] = pos[0] < 0 ? -1 : pos[0] + 32;
-                            break;
+                    for (int i = 0; i < 4; ++i) {
+                        if (i > 0 && i * 32 % box != 0) {  // within the box of the quarter before
+                            pos[i] = pos[i - 1] < 0 ? -1 : pos[i - 1] + 32;
+                            continue;
                         }
                         int p;  // key position of the box
                         if (a.ids) {
@@ -363,49 +510,51 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_attn_kernel(
                     }
                 }
                 const int m = min(32, x1 - xb);
-                for (int y = 0; y < m; ++y) {
-                    const int p0 = __shfl_sync(0xFFFFFFFFu, pos[0], y), p1 = __shfl_sync(0xFFFFFFFFu, pos[1], y);
-                    const int z0 = __shfl_sync(0xFFFFFFFFu, z[0], y), z1 = __shfl_sync(0xFFFFFFFFu, z[1], y);
+                for (int y = 0; y < m && ok; ++y) {
+                    int p[4], zz[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        p[i] = __shfl_sync(0xFFFFFFFFu, pos[i], y);
+                        zz[i] = __shfl_sync(0xFFFFFFFFu, z[i], y);
+                    }
                     const int st = it % T::STAGES;
                     if (lane == 0) {
                         if (it >= T::STAGES)
                             ok = mbar_wait(empty + st, ((it / T::STAGES) & 1) ^ 1, abort_flag, a.status);
                         if (ok) {
-                            meta[st].pos[0] = p0;
-                            meta[st].pos[1] = p1;
-                            unsigned char *dk = ring + st * T::STAGE, *dv = dk + T::BYTES;
-                            const int boxes = (p0 >= 0) + (half < kKeys && p1 >= 0);
-                            if (boxes == 0) {
-                                mbar_arrive(full + st);
-                            } else {
-                                mbar_arrive_expect_tx(full + st, boxes * half * (2 * D * (I8 ? 1 : 2) + (I8 ? 8 : 0)));
-                                for (int i = 0; i < kKeys / half; ++i) {
-                                    if ((i ? p1 : p0) < 0) continue;
-                                    const int zz = i ? z1 : z0;
+                            *reinterpret_cast<int4 *>(meta + st) = make_int4(p[0], p[1], p[2], p[3]);
+                            unsigned char *dv = ring + st * T::STAGE, *dk = dv + T::BYTES;
+                            int boxes = 0;
 #pragma unroll
-                                    for (int r = 0; r < T::REGS; ++r) {
-                                        const uint32_t o = r * T::REGION + i * half * T::ROWB;
-                                        tma_load_3d(dk + o, &tm_k, full + st, r * 64, walk.h, zz);
-                                        tma_load_3d(dv + o, &tm_v, full + st, r * 64, walk.h, zz);
-                                    }
-                                    if (I8) {
-                                        const int page = zz / block;
-                                        const long long so = (static_cast<long long>(page) * a.c.Hkv + walk.h) * block + (zz - page * block);
-                                        bulk_load(scales + st * 128 + i * half, a.c.k_scales + so, half * 4, full + st);
-                                        bulk_load(scales + st * 128 + 64 + i * half, a.c.v_scales + so, half * 4, full + st);
-                                    }
+                            for (int i = 0; i < 4; ++i) boxes += i * 32 % box == 0 && p[i] >= 0;
+                            if (boxes == 0)
+                                mbar_arrive(full + st);
+                            else
+                                mbar_arrive_expect_tx(full + st, boxes * box * (2 * D * T::EB + (I8 ? 8 : 0)));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (i * 32 % box != 0 || p[i] < 0) continue;
+#pragma unroll
+                                for (int r = 0; r < T::REGS; ++r) {
+                                    const uint32_t o = r * T::REGION + i * 32 * T::ROWB;
+                                    tma_load_3d(dk + o, &tm_k, full + st, r * 64, walk.h, zz[i]);
+                                    tma_load_3d(dv + o, &tm_v, full + st, r * 64, walk.h, zz[i]);
+                                }
+                                if (I8) {
+                                    const int page = zz[i] / block;
+                                    const long long so = (static_cast<long long>(page) * a.c.Hkv + walk.h) * block + (zz[i] - page * block);
+                                    bulk_load(scales + (2 * st) * kKeys + i * 32, a.c.k_scales + so, box * 4, full + st);
+                                    bulk_load(scales + (2 * st + 1) * kKeys + i * 32, a.c.v_scales + so, box * 4, full + st);
                                 }
                             }
                         }
                     }
                     ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-                    if (!ok) break;
-                    ++it;
+                    if (ok) ++it;
                 }
             }
         }
-        // the copies have landed before the CTA ends (after an abort; otherwise
-        // the compute warps have seen them all)
+        // after an abort: the copies have landed before the CTA ends
         if (!ok && lane == 0) {
             for (uint32_t i = it > T::STAGES ? it - T::STAGES : 0; i < it; ++i) {
                 const uint64_t t0 = global_timer_ns();
@@ -416,398 +565,322 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_attn_kernel(
         return;
     }
 
-    // ------------------------------------------------------------ compute
-    const int gq = lane >> 2, c = lane & 3;
-    uint32_t it = 0;
-    bool ok = true;  // false: a wait gave up; the warps still meet at every barrier
-    while (walk.next(a)) {
-        const RowTile t = row_tile(a, walk.s, walk.rt);
+    // ------------------------------------------------------------ warps 0-3
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, T::TMEM);
+        tmem_relinquish();
+    }
+    // rows of the operand buffers that no digit or head ever fills
+    for (int e = tid; e < T::QBYTES / 16; e += 128) reinterpret_cast<uint4 *>(q_s)[e] = make_uint4(0, 0, 0, 0);
+    tc_fence_before();
+    named_barrier(1, 128);
+    tc_fence_after();
+    const uint32_t tmem_s = *tmem_slot, tmem_o = tmem_s + T::NS;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    constexpr uint32_t idesc_s = I8 ? idesc_s8_s32(128, T::NS) : idesc_bf16_f32(128, T::NS, false);
+    constexpr uint32_t idesc_o = (I8 ? idesc_s8_s32(128, T::NO) : idesc_bf16_f32(128, T::NO, false)) | kIdescAMn;
+    constexpr int EK = I8 ? 32 : 16;  // contraction of one instruction (32 bytes)
+
+    uint32_t it = 0, n_s = 0;  // tiles taken; products of each kind awaited
+    bool ok = true;            // false: a wait of this thread gave up
+    bool dead = false;         // the same for all: no tile is taken any more, but every
+                               // barrier is met
+    while (walk.next(a, R)) {
+        const RowTile t = row_tile(a, walk.s, walk.rt, R);
         const int x1 = min(walk.x1, t.count);
         const bool whole = walk.x0 == 0 && walk.x1 == walk.s.nk;
-        // this thread's two rows: positions (-1: no such row) and Q fragments
-        int tpos[2];
-        uint32_t qf[T::KST][4];
+        // ---- Q rows into shared memory, 16 threads per row (8 with d = 64)
+        constexpr int TPR = D / 8;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = t.r0 + gq + 8 * i;
-            const int tok = r / a.G;
-            tpos[i] = r < t.rows ? walk.s.off + tok : -1;
-            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
-                                     (walk.s.cu0 + tok) * a.q_stride +
-                                     (static_cast<long long>(walk.h) * a.G + (r - tok * a.G)) * D;
+        for (int rr = 0; rr < R; rr += 128 / TPR) {
+            const int r = rr + tid / TPR, c = tid % TPR;
+            if (R % (128 / TPR) != 0 && r >= R) continue;  // (whole warps)
+            const int row = t.r0 + r, tok = row / a.G;
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (row < t.rows)
+                u = *reinterpret_cast<const uint4 *>(
+                    static_cast<const __nv_bfloat16 *>(a.q) + (walk.s.cu0 + tok) * a.q_stride +
+                    (static_cast<long long>(walk.h) * a.G + (row - tok * a.G)) * D + c * 8);
+            if (c == 0) {
+                rowpos[r] = row < t.rows ? walk.s.off + tok : -1;
+                maxima[r] = -INFINITY;
+                if (I8) poison[r] = 0;
+            }
             if (!I8) {
-#pragma unroll
-                for (int p = 0; p < T::KST / 2; ++p) {  // piece 2c + p % 2 of region p / 2
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    if (r < t.rows) u = *reinterpret_cast<const uint4 *>(q + (p / 2) * 64 + (2 * c + p % 2) * 8);
-                    qf[2 * p][i] = u.x;
-                    qf[2 * p][2 + i] = u.y;
-                    qf[2 * p + 1][i] = u.z;
-                    qf[2 * p + 1][2 + i] = u.w;
-                }
+                *reinterpret_cast<uint4 *>(q_s + (c / 8) * T::NS * 128 + sw128_offset(r, c % 8)) = u;
             } else {
+                // digits of q / 2^e, 2^e the largest power of two <= the row's largest |q|
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                      __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
 #pragma unroll
-                for (int p = 0; p < T::KST / 2; ++p) {  // 8 of the 16 values of a piece of codes
-                    const int piece = D == 128 ? 2 * c + p / 2 : c;
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    if (r < t.rows) u = *reinterpret_cast<const uint4 *>(q + piece * 16 + (p % 2) * 8);
-                    qf[2 * p][i] = u.x;
-                    qf[2 * p][2 + i] = u.y;
-                    qf[2 * p + 1][i] = u.z;
-                    qf[2 * p + 1][2 + i] = u.w;
+                for (int o = 1; o < TPR; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                const uint32_t top = max(m & 0xFFFFu, m >> 16) << 16;
+                const uint32_t e = top & 0x7F800000u;
+                const bool usable = e != 0 && e != 0x7F800000u;
+                // 2^-e as a product, since 2^-127 is subnormal: the biased exponents of the
+                // factors add up to 127 + 127 + (127 - biased e)
+                const uint32_t e1 = e >> 1 & 0x7F800000u;
+                const float inv = usable ? __uint_as_float(0x5F000000u - e1) : 0.f;
+                const float inv2 = usable ? __uint_as_float(0x5F800000u - (e - e1)) : 0.f;
+                if (c == 0)
+                    qscale[r] = e == 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                                                 : __uint_as_float(e) * 1.9073486328125e-6f * a.scale_log2;  // 2^-19
+                uint32_t d0[2] = {0, 0}, d1[2] = {0, 0}, d2[2] = {0, 0};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float q = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+                    const int x = usable ? __float2int_rn(q * inv * inv2 * 524288.f) : 0;  // |x| <= 2^20
+                    const int y0 = ((x + 64) & 127) - 64, x1_ = (x - y0) >> 7;
+                    const int y1 = ((x1_ + 64) & 127) - 64, y2 = (x1_ - y1) >> 7;
+                    d0[i / 4] |= (static_cast<uint32_t>(y0) & 0xFFu) << (8 * (i % 4));
+                    d1[i / 4] |= (static_cast<uint32_t>(y1) & 0xFFu) << (8 * (i % 4));
+                    d2[i / 4] |= (static_cast<uint32_t>(y2) & 0xFFu) << (8 * (i % 4));
                 }
+                const uint32_t half = (c & 1) * 8;
+                *reinterpret_cast<uint2 *>(q_s + piece_at<T::ROWB>(r, c / 2) + half) = make_uint2(d0[0], d0[1]);
+                *reinterpret_cast<uint2 *>(q_s + piece_at<T::ROWB>(R + r, c / 2) + half) = make_uint2(d1[0], d1[1]);
+                *reinterpret_cast<uint2 *>(q_s + piece_at<T::ROWB>(2 * R + r, c / 2) + half) = make_uint2(d2[0], d2[1]);
             }
         }
-        float o[T::NT][4];
+        fence_proxy_async_smem();
+        named_barrier(1, 128);
+
+        float o[R], l[R];  // this column's sums, this key lane's weights
 #pragma unroll
-        for (int j = 0; j < T::NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        for (int r = 0; r < R; ++r) o[r] = l[r] = 0.f;
+        const float *m = maxima;  // the rows' running maxima
         const int last = min(t.tmax, walk.s.cap - 1);  // last key that any row sees
 
-        for (int x = walk.x0; x < x1 && ok; ++x, ++it) {
+        for (int x = walk.x0; x < x1 && !dead; ++x) {
             const int st = it % T::STAGES;
-            if (lane == 0) ok = mbar_wait(full + st, (it / T::STAGES) & 1, abort_flag, a.status);
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-            if (!ok) break;
-            // (every lane observes the phase itself, which orders its reads)
-            mbar_try_wait(full + st, (it / T::STAGES) & 1);
-            const int base = meta[st].pos[warp >> 1];
-            const int p0 = base + (warp & 1) * 16;  // first of this warp's 16 keys
-            const unsigned char *ks = ring + st * T::STAGE, *vs = ks + T::BYTES;
-            const bool none = base < 0 || p0 > last ||
-                              (a.window && p0 >= a.sinks && p0 + 15 <= t.tmin - a.window);
-            if (!none) {
-                const bool all = p0 + 15 <= min(t.tmin, walk.s.cap - 1) &&
-                                 (!a.window || p0 > t.tmax - a.window || p0 + 15 < a.sinks);
-                float s[2][4];
+            ok = ok && mbar_wait(full + st, (it / T::STAGES) & 1, abort_flag, a.status);
+            unsigned char *vs = ring + st * T::STAGE, *ks = vs + T::BYTES;
+            if (tid == 0 && ok) {
+                tc_fence_after();
+                const uint32_t ka = smem_addr(ks), qa = smem_addr(q_s);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
-                    const uint32_t key = warp * 16 + h * 8 + gq;
-                    if (!I8) {
-#pragma unroll
-                        for (int p = 0; p < T::KST / 2; ++p) {
-                            const uint4 u = *reinterpret_cast<const uint4 *>(
-                                ks + (p / 2) * T::REGION + piece_at<T::ROWB>(key, 2 * c + p % 2));
-                            mma16816(s[h], qf[2 * p][0], qf[2 * p][1], qf[2 * p][2], qf[2 * p][3], u.x, u.y);
-                            mma16816(s[h], qf[2 * p + 1][0], qf[2 * p + 1][1], qf[2 * p + 1][2], qf[2 * p + 1][3], u.z, u.w);
-                        }
-                    } else {
-#pragma unroll
-                        for (int p = 0; p < T::KST / 4; ++p) {
-                            const uint4 u = *reinterpret_cast<const uint4 *>(
-                                ks + piece_at<T::ROWB>(key, D == 128 ? 2 * c + p : c));
-                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t b0 = s8x2_bf16(__byte_perm(w[e], 0, 0x1100));
-                                const uint32_t b1 = s8x2_bf16(__byte_perm(w[e], 0, 0x3322));
-                                const int k = 4 * p + e;
-                                mma16816(s[h], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b0, b1);
-                            }
-                        }
-                    }
+                for (int k = 0; k < D / EK; ++k) {
+                    const uint64_t kd = row_desc<T::ROWB>(ka + (k / 4) * T::REGION + (k % 4) * 32);
+                    const uint64_t qd = row_desc<T::ROWB>(qa + (k / 4) * T::NS * 128 + (k % 4) * 32);
+                    if (I8)
+                        umma_i8(tmem_s, kd, qd, idesc_s, k > 0);
+                    else
+                        umma_bf16(tmem_s, kd, qd, idesc_s, k > 0);
                 }
-                // scores in log2 units; masked ones are -inf whatever the key held
-                bool seen[2][4];
+                umma_commit(bar_s);
+            }
+            // this thread's key
+            const int base = ok ? meta[st].pos[warp] : -1;
+            const int pos = base < 0 ? 0x7FFFFFFF : base + lane;
+            const bool any = pos <= last && (!a.window || pos > t.tmin - a.window || pos < a.sinks);
+            const bool every = pos <= min(t.tmin, walk.s.cap - 1) && (!a.window || pos > t.tmax - a.window || pos < a.sinks);
+            float sk = 1.f, sv = 1.f;
+            bool bad_sv = false;
+            if (I8) {
+                sk = scales[2 * st * kKeys + tid];
+                sv = any ? scales[(2 * st + 1) * kKeys + tid] : 0.f;
+                bad_sv = !(sv <= 3.4028235e38f);  // inf or NaN
+                if (bad_sv) sv = 0.f;
+                const float top = warp_max(sv);
+                if (lane == 0) reinterpret_cast<float *>(tops + R)[warp] = top;
+            } else if (!any) {
+                // a key that no row sees counts nothing, whatever its V row holds
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float2 sk = make_float2(1.f, 1.f);
-                    if (I8) sk = *reinterpret_cast<const float2 *>(scales + st * 128 + warp * 16 + h * 8 + 2 * c);
+                for (int r = 0; r < T::REGS; ++r)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float y = s[h][e] * a.scale_log2;
-                        if (I8) y *= e & 1 ? sk.y : sk.x;
-                        bool v = true;
-                        if (!all) {
-                            const int pos = p0 + h * 8 + 2 * c + (e & 1), tt = tpos[e >> 1];
-                            v = pos <= min(tt, walk.s.cap - 1) &&
-                                (!a.window || pos > tt - a.window || pos < a.sinks);
-                        }
-                        seen[h][e] = v;
-                        s[h][e] = v ? y : -INFINITY;
-                    }
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4 *>(vs + r * T::REGION + tid * 128 + ((c + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            const bool all = __all_sync(0xFFFFFFFFu, every);
+            ok = ok && mbar_wait(bar_s, n_s & 1, abort_flag, a.status);
+            tc_fence_after();
+            float s[R];
+#pragma unroll
+            for (int r0 = 0; r0 < R; r0 += 8) {
+                uint32_t w[I8 ? 3 : 1][8];
+#pragma unroll
+                for (int i = 0; i < (I8 ? 3 : 1); ++i) tmem_ld8(tmem_s + lanes + i * R + r0, w[i]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    s[r0 + r] = I8 ? from_digits(w[0][r], w[I8][r], w[2 * I8][r]) * (qscale[r0 + r] * sk)
+                                   : __uint_as_float(w[0][r]) * a.scale_log2;
+            }
+            if (!all) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int tt = rowpos[r];
+                    const bool v = pos <= min(tt, walk.s.cap - 1) && (!a.window || pos > tt - a.window || pos < a.sinks);
+                    if (I8 && bad_sv && v) poison[r] = 1;
+                    s[r] = v ? s[r] : -INFINITY;
                 }
-                float g[2];
+            } else if (I8 && bad_sv) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    g[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-                    g[i] = fmaxf(g[i], __shfl_xor_sync(0xFFFFFFFFu, g[i], 1));
-                    g[i] = fmaxf(g[i], __shfl_xor_sync(0xFFFFFFFFu, g[i], 2));
+                for (int r = 0; r < R; ++r) poison[r] = 1;
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float g = warp_max(s[r]);
+                if (lane == 0) reinterpret_cast<float *>(tops + r)[warp] = g;
+            }
+            tc_fence_before();
+            dead = named_barrier_or(1, 128, !ok);
+            if (dead) break;
+            // ---- weights, relative to the running maxima
+            float svmax = 1.f, svr = 1.f;
+            if (I8) {
+                const float4 g = tops[R];
+                svmax = fmaxf(fmaxf(g.x, g.y), fmaxf(g.z, g.w));
+                svr = svmax > 1e-37f ? sv * __frcp_rn(svmax) : 0.f;
+            }
+            float *mnext = maxima + (m == maxima ? R : 0);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 g = tops[r];
+                const float mo = m[r], mn = fmaxf(fmaxf(fmaxf(g.x, g.y), fmaxf(g.z, g.w)), mo);
+                if (mn != mo) {  // (the same for all threads)
+                    const float f = mo == -INFINITY ? (l[r] == 0.f ? 0.f : 1.f) : ex2_approx(mo - mn);
+                    o[r] *= f;
+                    l[r] *= f;
                 }
-                // the reference m only has to keep the weights in range: it is
-                // raised (and o, l rescaled) when a score passes it by 2^8
-                if (__any_sync(0xFFFFFFFFu, g[0] > m[0] + 8.f || g[1] > m[1] + 8.f)) {
-                    float f[2];
+                if (tid == 0) mnext[r] = mn;
+                const float p = ex2_approx(s[r] - (mn == -INFINITY ? 0.f : mn));
+                l[r] += p;
+                if (I8) {
+                    const uint32_t y = __float2uint_rn(p * svr * 134217728.f);  // 2^27, at most
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float mn = fmaxf(m[i], g[i]);
-                        f[i] = m[i] == -INFINITY ? 0.f : ex2_approx(m[i] - mn);
-                        m[i] = mn;
-                        l[i] *= f[i];
-                    }
-#pragma unroll
-                    for (int j = 0; j < T::NT; ++j) {
-                        o[j][0] *= f[0];
-                        o[j][1] *= f[0];
-                        o[j][2] *= f[1];
-                        o[j][3] *= f[1];
-                    }
-                }
-                uint32_t hi[4], lo[4];  // A fragments of the weights
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float2 sv = make_float2(1.f, 1.f);
-                    if (I8) sv = *reinterpret_cast<const float2 *>(scales + st * 128 + 64 + warp * 16 + h * 8 + 2 * c);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float mr = m[i] == -INFINITY ? 0.f : m[i];
-                        float w0 = ex2_approx(s[h][2 * i] - mr), w1 = ex2_approx(s[h][2 * i + 1] - mr);
-                        l[i] += w0 + w1;
-                        if (I8) {  // (a masked key's scale may hold anything)
-                            w0 = seen[h][2 * i] ? w0 * sv.x : 0.f;
-                            w1 = seen[h][2 * i + 1] ? w1 * sv.y : 0.f;
-                        }
-                        const uint32_t p = bf2(w0, w1);
-                        hi[2 * h + i] = p;
-                        lo[2 * h + i] = bf2(w0 - __uint_as_float(p << 16), w1 - __uint_as_float(p & 0xFFFF0000u));
-                    }
-                }
-                // keys that no row of the tile sees count nothing, whatever their V rows hold
-                uint32_t keep[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int pos = p0 + (e >> 1) * 8 + 2 * c + (e & 1);
-                    const bool v = all || (pos <= last && (!a.window || pos > t.tmin - a.window || pos < a.sinks));
-                    keep[e] = v ? 0xFFFFFFFFu : 0u;
-                }
-                const uint32_t row = warp * 16 + 2 * c;
-#pragma unroll
-                for (int r = 0; r < (I8 ? 1 : T::REGS); ++r) {
-                    uint4 u[4];
-                    const unsigned char *vr = vs + r * T::REGION;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t k = row + (e >> 1) * 8 + (e & 1);
-                        if (I8 && D == 64) {
-                            const uint2 y = *reinterpret_cast<const uint2 *>(vr + piece_at<T::ROWB>(k, gq >> 1) + (gq & 1) * 8);
-                            u[e] = make_uint4(y.x, y.y, 0, 0);
-                        } else {
-                            u[e] = *reinterpret_cast<const uint4 *>(vr + piece_at<T::ROWB>(k, gq));
-                        }
-                        if (!I8) {
-                            u[e].x &= keep[e];
-                            u[e].y &= keep[e];
-                            u[e].z &= keep[e];
-                            u[e].w &= keep[e];
-                        }
-                    }
-                    const uint32_t w[4][4] = {{u[0].x, u[0].y, u[0].z, u[0].w},
-                                              {u[1].x, u[1].y, u[1].z, u[1].w},
-                                              {u[2].x, u[2].y, u[2].z, u[2].w},
-                                              {u[3].x, u[3].y, u[3].z, u[3].w}};
-#pragma unroll
-                    for (int j = 0; j < T::CW; ++j) {
-                        uint32_t b0, b1;
-                        if (!I8) {
-                            const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
-                            b0 = __byte_perm(w[0][j / 2], w[1][j / 2], sel);
-                            b1 = __byte_perm(w[2][j / 2], w[3][j / 2], sel);
-                        } else {
-                            const uint32_t e = j & 3, sel = e | (e << 4) | ((4 + e) << 8) | ((4 + e) << 12);
-                            b0 = s8x2_bf16(__byte_perm(w[0][j / 4], w[1][j / 4], sel));
-                            b1 = s8x2_bf16(__byte_perm(w[2][j / 4], w[3][j / 4], sel));
-                        }
-                        float(&acc)[4] = o[r * 8 + j];
-                        mma16816(acc, hi[0], hi[1], hi[2], hi[3], b0, b1);
-                        mma16816(acc, lo[0], lo[1], lo[2], lo[3], b0, b1);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        p_s[sw128_offset(i * R + r, tid / 16) + tid % 16] = static_cast<unsigned char>(y >> (7 * i) & 0x7Fu);
+                } else {
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(p), lo = __float2bfloat16_rn(p - __bfloat162float(hi));
+                    unsigned char *at = p_s + (tid / 64) * T::NO * 128 + tid % 8 * 2;
+                    *reinterpret_cast<__nv_bfloat16 *>(at + sw128_offset(r, tid % 64 / 8)) = hi;
+                    *reinterpret_cast<__nv_bfloat16 *>(at + sw128_offset(R + r, tid % 64 / 8)) = lo;
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + st);
+            m = mnext;
+            fence_proxy_async_smem();
+            named_barrier(1, 128);
+            if (tid == 0) {
+                tc_fence_after();
+                const uint32_t va = smem_addr(vs), pa = smem_addr(p_s);
+#pragma unroll
+                for (int k = 0; k < kKeys / EK; ++k) {
+                    const uint64_t vd = col_desc<T::ROWB, T::REGION>(va + k * EK * T::ROWB);
+                    const uint64_t pd = row_desc<128>(pa + (k / 4) * T::NO * 128 + (k % 4) * 32);
+                    if (I8)
+                        umma_i8(tmem_o, vd, pd, idesc_o, k > 0);
+                    else
+                        umma_bf16(tmem_o, vd, pd, idesc_o, k > 0);
+                }
+                umma_commit(bar_o);
+            }
+            ok = mbar_wait(bar_o, n_s & 1, abort_flag, a.status);  // (ok: the barrier saw it)
+            ++n_s;
+            tc_fence_after();
+            const float unit = svmax * 7.450580596923828e-9f;  // 2^-27
+#pragma unroll
+            for (int r0 = 0; r0 < R; r0 += 8) {
+                uint32_t w[I8 ? 4 : 2][8];
+#pragma unroll
+                for (int i = 0; i < (I8 ? 4 : 2); ++i) tmem_ld8(tmem_o + lanes + i * R + r0, w[i]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    o[r0 + r] = I8 ? fmaf(from_digits(w[0][r], w[1][r], w[2 * I8][r] + 128 * w[3 * I8][r]), unit, o[r0 + r])
+                                   : o[r0 + r] + (__uint_as_float(w[0][r]) + __uint_as_float(w[1][r]));
+            }
+            tc_fence_before();
+            if (tid == 0) mbar_arrive(empty + st);  // (thread 0 saw both products complete)
+            ++it;
         }
 
-        // ---- the four warps' results of the segment, merged
+        // ---- end of the segment: the rows' sums over the 128 key lanes
+        named_barrier(1, 128);  // (the last tile's reads of tops are done)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-            if (c == 0) ml[warp * kTileRows + gq + 8 * i] = make_float2(m[i], l[i]);
+        for (int r = 0; r < R; ++r) {
+            float y = l[r];
+#pragma unroll
+            for (int k = 16; k; k >>= 1) y += __shfl_xor_sync(0xFFFFFFFFu, y, k);
+            if (lane == 0) reinterpret_cast<float *>(tops + r)[warp] = y;
         }
-        named_barrier(1, 32 * kComputeWarps);
-        float f[2];
+        named_barrier(1, 128);
+        const bool lead = walk.pos - (walk.x1 - walk.x0) == found.start;  // the run's first piece
+        const long long prow = (2ll * blockIdx.x + (lead ? 0 : 1)) * R;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float top = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kComputeWarps; ++w) top = fmaxf(top, ml[w * kTileRows + gq + 8 * i].x);
-            f[i] = m[i] == -INFINITY ? (l[i] == 0.f ? 0.f : 1.f) : ex2_approx(m[i] - top);
-        }
-        // this thread's row and 4 columns of each 32-column round
-        const int row = tid >> 3, n = tid & 7;
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kComputeWarps; ++w) top = fmaxf(top, ml[w * kTileRows + row].x);
-#pragma unroll
-        for (int w = 0; w < kComputeWarps; ++w) {
-            const float2 y = ml[w * kTileRows + row];
-            sum += y.x == -INFINITY ? y.y : y.y * ex2_approx(y.x - top);
-        }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const float lse2 = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) + __log2f(sum);
-        const int r = t.r0 + row, tok = r / a.G;
-        const bool live = r < t.rows;
-        const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (r - tok * a.G);
-        const long long prow = (2ll * blockIdx.x + (walk.pos - (walk.x1 - walk.x0) == start ? 0 : 1)) * kTileRows + row;
-        if (n == 0 && live) {
-            if (whole)
-                a.lse[orow] = lse2 * kLn2f;
-            else
-                a.part_lse[prow] = lse2;
-        }
-#pragma unroll
-        for (int q = 0; q < T::NT / 4; ++q) {
-            // columns of 8-column tiles 4q .. 4q + 3: value e of group n is column
-            // (region) * 64 + n * CW + (first of the four) + e
-            float *mine = merge + (warp * kTileRows + gq) * 32 + 2 * c * 4;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    *reinterpret_cast<float4 *>(mine + i * 8 * 32 + k * 4) =
-                        make_float4(o[4 * q][2 * i + k] * f[i], o[4 * q + 1][2 * i + k] * f[i],
-                                    o[4 * q + 2][2 * i + k] * f[i], o[4 * q + 3][2 * i + k] * f[i]);
-            named_barrier(1, 32 * kComputeWarps);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kComputeWarps; ++w) {
-                const float4 y = *reinterpret_cast<const float4 *>(merge + (w * kTileRows + row) * 32 + n * 4);
-                acc.x += y.x;
-                acc.y += y.y;
-                acc.z += y.z;
-                acc.w += y.w;
+        for (int r = 0; r < R; ++r) {
+            const int row = t.r0 + r;
+            if (row >= t.rows) break;
+            const float4 y = tops[r];
+            const float sum = (y.x + y.y) + (y.z + y.w);
+            float inv = sum == 0.f ? 0.f : 1.f / sum;
+            if (I8 && poison[r]) inv = __uint_as_float(0x7FC00000u);
+            const float lse2 = sum == 0.f ? -INFINITY : (m[r] == -INFINITY ? 0.f : m[r]) + __log2f(sum);
+            if (whole) {
+                const int tok = row / a.G;
+                const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq +
+                                       static_cast<long long>(walk.h) * a.G + (row - tok * a.G);
+                if (tid < D) static_cast<__nv_bfloat16 *>(a.out)[orow * D + tid] = __float2bfloat16_rn(o[r] * inv);
+                if (tid == 0) a.lse[orow] = lse2 * kLn2f;
+            } else {
+                if (tid < D) a.part_o[(prow + r) * D + tid] = o[r] * inv;
+                if (tid == 0) a.part_lse[prow + r] = lse2;
             }
-            const int col = I8 ? n * T::CW + 4 * q : (q / 2) * 64 + n * 8 + (q % 2) * 4;
-            if (live) {
-                if (whole)
-                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + col) =
-                        make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
-                else
-                    *reinterpret_cast<float4 *>(a.part_o + prow * D + col) =
-                        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        }
+        if (!whole) {
+            // pieces of this segment: one per run that holds a part of it
+            const long long seg0 = walk.pos - walk.x1, seg1 = seg0 + walk.s.nk;
+            const int c0 = static_cast<int>(seg0 / found.run), c1 = static_cast<int>((seg1 - 1) / found.run);
+            __threadfence();
+            named_barrier(1, 128);
+            if (tid == 0) *last_piece = atomicAdd(a.counters + c0, 1) == c1 - c0;
+            named_barrier(1, 128);
+            if (*last_piece) {
+                __threadfence();
+                merge_pieces<D, R>(a, t, walk.s.cu0, walk.h, c0, c1, seg0 == c0 * found.run,
+                                   reinterpret_cast<float *>(p_s));
+                if (tid == 0) a.counters[c0] = 0;  // as the next call expects it
             }
-            named_barrier(1, 32 * kComputeWarps);
+        } else {
+            named_barrier(1, 128);  // tops and the Q buffer are free
         }
     }
+    named_barrier(1, 128);
+    if (warp == 0) tmem_dealloc(tmem_s, T::TMEM);
 }
 
-// ===========================================================================
-// Merge of the segments that lie in several runs: CTA c takes the segment
-// that begins in run c and goes on into run c + 1, if there is one.  Its
-// pieces are the last one of run c and the first ones of the runs behind it.
-//   lse = log2 sum 2^lse_p,  out = sum 2^(lse_p - lse) o_p
-// ===========================================================================
-constexpr int kCombineThreads = 256;
-
-template <int D>
-__global__ void __launch_bounds__(kCombineThreads) split_combine_kernel(const __grid_constant__ PagedAttn a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces come from the previous kernel
-    __shared__ long long scan[10];
-    __shared__ float wt[32][kTileRows];
-    const long long work = total_work(a, scan);
-    const long long run = run_length(work, gridDim.x);
-    const long long first = run * blockIdx.x, next = first + run;
-    if (next >= work) return;
-    const Found at = find_unit(a, next - 1, scan);
-    const Seq s = seq_of(a, at.b);
-    const long long seg = at.off / s.nk;
-    const long long seg0 = next - 1 - (at.off - seg * s.nk), seg1 = seg0 + s.nk;
-    if (seg0 < first || seg1 <= next) return;  // begun earlier, or ends here
-    const int rt = static_cast<int>(seg / a.c.Hkv), h = static_cast<int>(seg - static_cast<long long>(rt) * a.c.Hkv);
-    const int pieces = static_cast<int>((seg1 - 1) / run - blockIdx.x) + 1;
-    const long long slot0 = 2ll * blockIdx.x + (seg0 == first ? 0 : 1);
-    auto slot = [&](int p) { return p == 0 ? slot0 : 2ll * (blockIdx.x + p); };
-
-    constexpr int COLS = D / 16;  // columns per thread
-    const int row = threadIdx.x >> 4, col = (threadIdx.x & 15) * COLS;
-    float acc[COLS];
-#pragma unroll
-    for (int e = 0; e < COLS; ++e) acc[e] = 0.f;
-    float top = -INFINITY, sum = 0.f;
-    for (int p0 = 0; p0 < pieces; p0 += 32) {
-        const int m = min(32, pieces - p0);
-        __syncthreads();
-        for (int e = threadIdx.x; e < m * kTileRows; e += kCombineThreads)
-            wt[e / kTileRows][e % kTileRows] = a.part_lse[slot(p0 + e / kTileRows) * kTileRows + e % kTileRows];
-        __syncthreads();
-        float g = top;
-        for (int p = 0; p < m; ++p) g = fmaxf(g, wt[p][row]);
-        const float f = top == -INFINITY ? 0.f : ex2_approx(top - g);
-        sum *= f;
-#pragma unroll
-        for (int e = 0; e < COLS; ++e) acc[e] *= f;
-        top = g;
-#pragma unroll 4
-        for (int p = 0; p < m; ++p) {
-            const float lp = wt[p][row];
-            if (lp == -INFINITY) continue;  // a piece without a key for this row
-            const float w = ex2_approx(lp - top);
-            const float4 *src = reinterpret_cast<const float4 *>(a.part_o + (slot(p0 + p) * kTileRows + row) * D + col);
-            sum += w;
-#pragma unroll
-            for (int e = 0; e < COLS / 4; ++e) {
-                const float4 y = src[e];
-                acc[4 * e] += w * y.x;
-                acc[4 * e + 1] += w * y.y;
-                acc[4 * e + 2] += w * y.z;
-                acc[4 * e + 3] += w * y.w;
-            }
-        }
-    }
-    const int r = rt * kTileRows + row;
-    if (r >= s.n * a.G) return;
-    const int tok = r / a.G;
-    const long long orow = (static_cast<long long>(s.cu0) + tok) * a.Hq + static_cast<long long>(h) * a.G + (r - tok * a.G);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + orow * D + col;
-#pragma unroll
-    for (int e = 0; e < COLS; e += 4)
-        *reinterpret_cast<uint2 *>(out + e) = make_uint2(bf2(acc[e] * inv, acc[e + 1] * inv),
-                                                         bf2(acc[e + 2] * inv, acc[e + 3] * inv));
-    if (col == 0) a.lse[orow] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2f;
+template <int D, bool I8, int R>
+cudaError_t launch(const PagedAttn &a, const CUtensorMap &tk, const CUtensorMap &tv, int num_sms,
+                   cudaStream_t st) {
+    using T = Tile<D, I8, R>;
+    constexpr size_t smem = split_smem_bytes<D, I8, R>();
+    static_assert(T::CTAS * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
+    const cudaError_t e = cudaFuncSetAttribute(
+        split_attn_kernel<D, I8, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int ctas = T::CTAS * num_sms < kSplitMaxCtas ? T::CTAS * num_sms : kSplitMaxCtas;
+    split_attn_kernel<D, I8, R><<<ctas, kThreads, smem, st>>>(tk, tv, a);
+    return cudaGetLastError();
 }
 
 template <int D, bool I8>
-cudaError_t launch(const PagedAttn &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
-                   cudaStream_t st) {
-    constexpr size_t smem = split_smem_bytes<D, I8>();
-    cudaError_t e = cudaFuncSetAttribute(split_attn_kernel<D, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    split_attn_kernel<D, I8><<<ctas, kSplitThreads, smem, st>>>(tk, tv, a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kCombineThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, split_combine_kernel<D>, a);
+cudaError_t launch_rows(const PagedAttn &a, int rows, const CUtensorMap &tk, const CUtensorMap &tv,
+                        int num_sms, cudaStream_t st) {
+    if (rows <= 8) return launch<D, I8, 8>(a, tk, tv, num_sms, st);
+    if (rows <= 16) return launch<D, I8, 16>(a, tk, tv, num_sms, st);
+    return launch<D, I8, 32>(a, tk, tv, num_sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_split_attn(const PagedAttn &a, const CUtensorMap &tk, const CUtensorMap &tv,
-                              int num_sms, cudaStream_t st) {
-    const int ctas = 2 * num_sms < kSplitMaxCtas ? 2 * num_sms : kSplitMaxCtas;
+cudaError_t launch_split_attn(const PagedAttn &a, int rows, const CUtensorMap &tk,
+                              const CUtensorMap &tv, int num_sms, cudaStream_t st) {
     if (a.c.d == 128)
-        return a.c.k_scales ? launch<128, true>(a, tk, tv, ctas, st) : launch<128, false>(a, tk, tv, ctas, st);
-    return a.c.k_scales ? launch<64, true>(a, tk, tv, ctas, st) : launch<64, false>(a, tk, tv, ctas, st);
+        return a.c.k_scales ? launch_rows<128, true>(a, rows, tk, tv, num_sms, st)
+                            : launch_rows<128, false>(a, rows, tk, tv, num_sms, st);
+    return a.c.k_scales ? launch_rows<64, true>(a, rows, tk, tv, num_sms, st)
+                        : launch_rows<64, false>(a, rows, tk, tv, num_sms, st);
 }
 
 }  // namespace msa

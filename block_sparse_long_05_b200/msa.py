@@ -159,8 +159,11 @@ def workspace_size(Bt, n_q, T, Hq, Hkv, d, d_idx, block, K, kv_group=None) -> in
     return int(lib.msa_workspace_size_kv_group(Bt, n_q, T, Hq, Hkv, d, d_idx, block, K, kv_group))
 
 
+HEADER_BYTES = 2304  # MSA_WORKSPACE_HEADER_BYTES
+
+
 class Workspace:
-    """Device scratch for the calls (status word zeroed at creation)."""
+    """Device scratch for the calls (its header zeroed at creation)."""
 
     def __init__(self, nbytes: int, device=None):
         if nbytes <= 0:
@@ -168,12 +171,10 @@ class Workspace:
         self.buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device or "cuda")
         off = (-self.buf.data_ptr()) % 256
         self.view = self.buf[off:off + nbytes]
-        self.view[:256].zero_()
+        self.view[:HEADER_BYTES].zero_()
         self.nbytes = nbytes
-
-    @property
-    def ptr(self) -> int:
-        return self.view.data_ptr()
+        self.ptr = self.view.data_ptr()
+        self.device_index = self.view.get_device()
 
     @classmethod
     def for_shape(cls, Bt, n_q, T, Hq, Hkv, d, d_idx, block, K, device=None,
@@ -363,95 +364,99 @@ def sparse_attn_decode_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     return out, lse
 
 
-class _Call:
-    """Device and stream of a paged-cache call: every tensor must live on one
-    device, which is made current for the launch; the stream defaults to that
-    device's current one."""
-
-    def __init__(self, ws: Workspace, stream, **tensors):
-        self.device = ws.view.device
-        for name, t in tensors.items():
-            if t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, the workspace on {self.device}")
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        self.stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-    def __call__(self, fn: str, *args):
-        call = getattr(load_library(), fn)
-        if self.device.index == torch.cuda.current_device():
-            _check(fn, call(*args, self.stream))
-        else:
-            with torch.cuda.device(self.device):
-                _check(fn, call(*args, self.stream))
+# The paged-cache calls are short and called once per layer and token, so their
+# binding keeps to few Python operations per tensor: one check each, against
+# the workspace's device, and one flat foreign call.
+_BF16, _I8, _I32, _F32 = torch.bfloat16, torch.int8, torch.int32, torch.float32
 
 
-def _rows(t: torch.Tensor, name: str, dims: int) -> int:
+def _refuse(t: torch.Tensor, dtype, device: int, name: str):
+    _dev(t, dtype, name)
+    raise ValueError(f"{name} is on {t.device}, the workspace on cuda:{device}")
+
+
+def _on(t: torch.Tensor, dtype, device: int, name: str) -> int:
+    """Address of a contiguous tensor of this type on the workspace's device."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, dtype, device, name)
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, device: int, name: str, dims: int) -> int:
     """Elements between the rows of a packed bf16 tensor whose rows are contiguous."""
-    if t.dtype != torch.bfloat16 or t.dim() != dims:
+    if t.dtype is not _BF16 or t.dim() != dims:
         raise ValueError(f"{name} must be a bfloat16 tensor of {dims} dimensions")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the workspace on cuda:{device}")
+    shape, stride = t.shape, t.stride()
     width = 1
     for i in range(dims - 1, 0, -1):
-        if t.shape[i] != 1 and t.stride(i) != width:
+        if stride[i] != width and shape[i] != 1:
             raise ValueError(f"{name}: each row must be contiguous")
-        width *= t.shape[i]
-    return t.stride(0) if t.shape[0] > 1 else width
+        width *= shape[i]
+    return stride[0] if shape[0] > 1 else width
 
 
-def _stores(k_pages, v_pages, k_scales=None, v_scales=None):
-    """(num_pages, block, Hkv, d) of a checked pair of page stores."""
-    dtype = torch.bfloat16 if k_scales is None else torch.int8
-    _dev(k_pages, dtype, "k_pages")
-    _dev(v_pages, dtype, "v_pages")
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+def _stores(k_pages, v_pages, k_scales, v_scales, dtype, device: int):
+    """Shape and addresses of a checked pair of page stores (and their scales)."""
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [num_pages, block, Hkv, d]")
-    if k_scales is not None:
-        pages, block, Hkv, _ = k_pages.shape
-        for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-            _dev(t, torch.float32, name)
-            if t.shape != (pages, Hkv, block):
-                raise ValueError(f"{name} must be [num_pages, Hkv, block]")
-    return k_pages.shape
+    at = (_on(k_pages, dtype, device, "k_pages"), _on(v_pages, dtype, device, "v_pages"))
+    if dtype is _I8:
+        want = (shape[0], shape[2], shape[1])
+        if k_scales.shape != want or v_scales.shape != want:
+            raise ValueError("k_scales and v_scales must be [num_pages, Hkv, block]")
+        at += (_on(k_scales, _F32, device, "k_scales"), _on(v_scales, _F32, device, "v_scales"))
+    return shape, at
 
 
-def _step(page_table, cu, kv_len) -> int:
-    """Bt of a checked step description."""
-    _dev(page_table, torch.int32, "page_table")
-    _dev(cu, torch.int32, "cu")
-    _dev(kv_len, torch.int32, "kv_len")
-    Bt = kv_len.shape[0] if kv_len.dim() == 1 else -1
-    if page_table.dim() != 2 or page_table.shape[0] != Bt or cu.shape != (Bt + 1,):
+def _step(page_table, cu, kv_len, num_pages: int, device: int):
+    """Bt and the arguments page_table, page_stride, num_pages, cu, kv_len."""
+    shape, Bt = page_table.shape, kv_len.shape[0] if kv_len.dim() == 1 else -1
+    if len(shape) != 2 or shape[0] != Bt or cu.shape != (Bt + 1,):
         raise ValueError("page_table must be [Bt, page_stride], cu [Bt + 1], kv_len [Bt]")
-    return Bt
+    return Bt, (_on(page_table, _I32, device, "page_table"), shape[1], num_pages,
+                _on(cu, _I32, device, "cu"), _on(kv_len, _I32, device, "kv_len"))
 
 
-def _append(fn, k, v, k_pages, v_pages, scales, page_table, cu, kv_len, ws, k_idx, k_idx_pages,
-            stream):
-    num_pages, block, Hkv, d = _stores(k_pages, v_pages, *scales)
-    Bt = _step(page_table, cu, kv_len)
-    ks, vs = _rows(k, "k", 3), _rows(v, "v", 3)
-    if k.shape != v.shape or k.shape[1:] != (Hkv, d):
+def _call(fn: str, ws: Workspace, stream, *args):
+    """The call on the workspace's device and that device's current stream."""
+    device = ws.device_index
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    call = getattr(_lib or load_library(), fn)
+    if torch._C._cuda_getDevice() == device:
+        code = call(*args, ws.ptr, ws.nbytes, stream)
+    else:
+        with torch.cuda.device(device):
+            code = call(*args, ws.ptr, ws.nbytes, stream)
+    if code:
+        raise MSAError(fn, code)
+
+
+def _append(fn, dtype, k, v, k_pages, v_pages, k_scales, v_scales, page_table, cu, kv_len, ws,
+            k_idx, k_idx_pages, stream):
+    dev = ws.device_index
+    (num_pages, block, Hkv, d), pages = _stores(k_pages, v_pages, k_scales, v_scales, dtype, dev)
+    Bt, step = _step(page_table, cu, kv_len, num_pages, dev)
+    ks, vs = _rows(k, dev, "k", 3), _rows(v, dev, "v", 3)
+    total = k.shape[0]
+    if k.shape != (total, Hkv, d) or v.shape != (total, Hkv, d):
         raise ValueError("k and v must be [total, Hkv, d]")
-    total, d_idx, xs, xp, xpp = k.shape[0], 0, 0, None, None
-    on = dict(k=k, v=v, k_pages=k_pages, v_pages=v_pages, page_table=page_table, cu=cu,
-              kv_len=kv_len)
-    if scales:
-        on.update(k_scales=scales[0], v_scales=scales[1])
-    if (k_idx is None) != (k_idx_pages is None):
-        raise ValueError("k_idx and k_idx_pages go together")
-    if k_idx is not None:
-        _dev(k_idx_pages, torch.bfloat16, "k_idx_pages")
-        xs, d_idx = _rows(k_idx, "k_idx", 2), k_idx.shape[1]
+    d_idx, xs, xp, xpp = 0, 0, None, None
+    if k_idx is not None or k_idx_pages is not None:
+        if k_idx is None or k_idx_pages is None:
+            raise ValueError("k_idx and k_idx_pages go together")
+        xs, xpp = _rows(k_idx, dev, "k_idx", 2), _on(k_idx_pages, _BF16, dev, "k_idx_pages")
+        xp, d_idx = k_idx.data_ptr(), k_idx.shape[1]
         if k_idx.shape[0] != total or k_idx_pages.shape != (num_pages, block, d_idx):
             raise ValueError("k_idx must be [total, d_idx], k_idx_pages [num_pages, block, d_idx]")
-        on.update(k_idx=k_idx, k_idx_pages=k_idx_pages)
-        xp, xpp = k_idx.data_ptr(), k_idx_pages.data_ptr()
-    run = _Call(ws, stream, **on)
     if total:  # (a step without rows has nothing to write, and no pointers to check)
-        run(fn, k.data_ptr(), ks, v.data_ptr(), vs, xp, xs, k_pages.data_ptr(), v_pages.data_ptr(),
-            *(t.data_ptr() for t in scales), xpp, page_table.data_ptr(), page_table.shape[1],
-            num_pages, cu.data_ptr(), kv_len.data_ptr(), Bt, total, Hkv, d, d_idx, block, ws.ptr,
-            ws.nbytes)
+        _call(fn, ws, stream, k.data_ptr(), ks, v.data_ptr(), vs, xp, xs, *pages, xpp, *step, Bt,
+              total, Hkv, d, d_idx, block)
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -462,8 +467,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: 
     may be strided), k_pages / v_pages [num_pages, block, Hkv, d] bf16, page_table
     [Bt, page_stride], cu [Bt + 1], kv_len [Bt] int32; optionally the index keys k_idx
     [total, d_idx] into k_idx_pages [num_pages, block, d_idx]."""
-    _append("msa_kv_append", k, v, k_pages, v_pages, (), page_table, cu, kv_len, ws, k_idx,
-            k_idx_pages, stream)
+    _append("msa_kv_append", _BF16, k, v, k_pages, v_pages, None, None, page_table, cu, kv_len, ws,
+            k_idx, k_idx_pages, stream)
 
 
 def kv_append_i8(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -473,31 +478,25 @@ def kv_append_i8(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
                  stream=None) -> None:
     """kv_append into int8 pages with a scale per (token, kv head) row
     (msa_kv_append_i8): k_scales / v_scales [num_pages, Hkv, block] fp32."""
-    _append("msa_kv_append_i8", k, v, k_pages, v_pages, (k_scales, v_scales), page_table, cu,
+    _append("msa_kv_append_i8", _I8, k, v, k_pages, v_pages, k_scales, v_scales, page_table, cu,
             kv_len, ws, k_idx, k_idx_pages, stream)
 
 
-def _gather(fn, k_pages, v_pages, scales, page_table, cu, kv_len, total, ws, k, v, stream):
-    num_pages, block, Hkv, d = _stores(k_pages, v_pages, *scales)
-    Bt = _step(page_table, cu, kv_len)
+def _gather(fn, dtype, k_pages, v_pages, k_scales, v_scales, page_table, cu, kv_len, total, ws, k,
+            v, stream):
+    dev = ws.device_index
+    (num_pages, block, Hkv, d), pages = _stores(k_pages, v_pages, k_scales, v_scales, dtype, dev)
+    Bt, step = _step(page_table, cu, kv_len, num_pages, dev)
+    shape = (total, Hkv, d)
     if k is None:
-        k = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=k_pages.device)
+        k = torch.empty(shape, dtype=_BF16, device=k_pages.device)
     if v is None:
-        v = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=k_pages.device)
-    _dev(k, torch.bfloat16, "k")
-    _dev(v, torch.bfloat16, "v")
-    if k.shape != (total, Hkv, d) or v.shape != k.shape:
+        v = torch.empty_like(k)
+    kp, vp = _on(k, _BF16, dev, "k"), _on(v, _BF16, dev, "v")
+    if k.shape != shape or v.shape != shape:
         raise ValueError("k and v must be [total, Hkv, d]")
-    on = dict(k=k, v=v, k_pages=k_pages, v_pages=v_pages, page_table=page_table, cu=cu,
-              kv_len=kv_len)
-    if scales:
-        on.update(k_scales=scales[0], v_scales=scales[1])
-    run = _Call(ws, stream, **on)
     if total:
-        run(fn, k_pages.data_ptr(), v_pages.data_ptr(), *(t.data_ptr() for t in scales),
-            page_table.data_ptr(), page_table.shape[1], num_pages, cu.data_ptr(),
-            kv_len.data_ptr(), k.data_ptr(), v.data_ptr(), Bt, total, Hkv, d, block, ws.ptr,
-            ws.nbytes)
+        _call(fn, ws, stream, *pages, *step, kp, vp, Bt, total, Hkv, d, block)
     return k, v
 
 
@@ -506,8 +505,8 @@ def kv_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Te
               k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
     """Cached rows of a step's positions as packed bf16 (msa_kv_gather):
     -> (k, v) [total, Hkv, d].  Rows behind cu[Bt] are left as they were."""
-    return _gather("msa_kv_gather", k_pages, v_pages, (), page_table, cu, kv_len, total, ws, k, v,
-                   stream)
+    return _gather("msa_kv_gather", _BF16, k_pages, v_pages, None, None, page_table, cu, kv_len,
+                   total, ws, k, v, stream)
 
 
 def kv_gather_i8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
@@ -515,41 +514,33 @@ def kv_gather_i8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.T
                  kv_len: torch.Tensor, total: int, ws: Workspace, k: torch.Tensor | None = None,
                  v: torch.Tensor | None = None, stream=None):
     """kv_gather from int8 pages (msa_kv_gather_i8): code * scale, rounded once."""
-    return _gather("msa_kv_gather_i8", k_pages, v_pages, (k_scales, v_scales), page_table, cu,
+    return _gather("msa_kv_gather_i8", _I8, k_pages, v_pages, k_scales, v_scales, page_table, cu,
                    kv_len, total, ws, k, v, stream)
 
 
-def _outputs(q, shape, out, lse):
+def _outputs(q, shape, out, lse, device: int):
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = q.new_empty(shape)
     if lse is None:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
-    _dev(out, torch.bfloat16, "out")
-    _dev(lse, torch.float32, "lse")
+        lse = torch.empty(shape[:-1], dtype=_F32, device=q.device)
     if out.shape != shape or lse.shape != shape[:-1]:
         raise ValueError("out / lse shapes do not match q")
-    return out, lse
+    return out, lse, _on(out, _BF16, device, "out"), _on(lse, _F32, device, "lse")
 
 
-def _attend(fn, q, k_pages, v_pages, scales, page_table, cu, kv_len, ws, window, sinks, max_q, out,
-            lse, stream):
-    num_pages, block, Hkv, d = _stores(k_pages, v_pages, *scales)
-    Bt = _step(page_table, cu, kv_len)
-    q_stride = _rows(q, "q", 3)
-    total, Hq, d2 = q.shape
+def _attend(fn, dtype, q, k_pages, v_pages, k_scales, v_scales, page_table, cu, kv_len, ws, window,
+            sinks, max_q, out, lse, stream):
+    dev = ws.device_index
+    (num_pages, block, Hkv, d), pages = _stores(k_pages, v_pages, k_scales, v_scales, dtype, dev)
+    Bt, step = _step(page_table, cu, kv_len, num_pages, dev)
+    q_stride, shape = _rows(q, dev, "q", 3), q.shape
+    total, Hq, d2 = shape
     if d2 != d:
         raise ValueError("q must be [total, Hq, d]")
-    out, lse = _outputs(q, q.shape, out, lse)
-    on = dict(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, cu=cu, kv_len=kv_len,
-              out=out, lse=lse)
-    if scales:
-        on.update(k_scales=scales[0], v_scales=scales[1])
-    run = _Call(ws, stream, **on)
+    out, lse, op, lp = _outputs(q, shape, out, lse, dev)
     if total:
-        run(fn, q.data_ptr(), q_stride, k_pages.data_ptr(), v_pages.data_ptr(),
-            *(t.data_ptr() for t in scales), page_table.data_ptr(), page_table.shape[1], num_pages,
-            cu.data_ptr(), kv_len.data_ptr(), out.data_ptr(), lse.data_ptr(), Bt, total, max_q or 0,
-            Hq, Hkv, d, block, window, sinks, ws.ptr, ws.nbytes)
+        _call(fn, ws, stream, q.data_ptr(), q_stride, *pages, *step, op, lp, Bt, total, max_q or 0,
+              Hq, Hkv, d, block, window, sinks)
     return out, lse
 
 
@@ -562,8 +553,8 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     [num_pages, block, Hkv, d] bf16 -> (out [total, Hq, d] bf16, lse [total, Hq] fp32).
     window > 0: each query sees the last `window` keys and the first `sinks` ones.
     max_q: the largest number of rows of one sequence, if known (it chooses kernels)."""
-    return _attend("msa_attn_paged", q, k_pages, v_pages, (), page_table, cu, kv_len, ws, window,
-                   sinks, max_q, out, lse, stream)
+    return _attend("msa_attn_paged", _BF16, q, k_pages, v_pages, None, None, page_table, cu,
+                   kv_len, ws, window, sinks, max_q, out, lse, stream)
 
 
 def attn_paged_i8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -572,8 +563,8 @@ def attn_paged_i8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                   sinks: int = 0, max_q: int | None = None, out: torch.Tensor | None = None,
                   lse: torch.Tensor | None = None, stream=None):
     """attn_paged over int8 pages with their scales (msa_attn_paged_i8)."""
-    return _attend("msa_attn_paged_i8", q, k_pages, v_pages, (k_scales, v_scales), page_table, cu,
-                   kv_len, ws, window, sinks, max_q, out, lse, stream)
+    return _attend("msa_attn_paged_i8", _I8, q, k_pages, v_pages, k_scales, v_scales, page_table,
+                   cu, kv_len, ws, window, sinks, max_q, out, lse, stream)
 
 
 def sparse_attn_paged_i8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -583,22 +574,18 @@ def sparse_attn_paged_i8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     """Decode sparse branch over int8 pages (msa_sparse_attn_paged_i8): q [Bt, 1, Hq, d]
     bf16, ids [Bt, 1, K] int32 -> (out [Bt, 1, Hq, d] bf16, lse [Bt, 1, Hq] fp32).  ws is
     a cache workspace (Workspace.for_cache)."""
-    num_pages, block, Hkv, d = _stores(k_pages, v_pages, k_scales, v_scales)
-    _dev(q, torch.bfloat16, "q")
-    _dev(page_table, torch.int32, "page_table")
-    _dev(ids, torch.int32, "ids")
-    Bt, n_q, Hq, d2 = q.shape
+    dev = ws.device_index
+    (num_pages, block, Hkv, d), pages = _stores(k_pages, v_pages, k_scales, v_scales, _I8, dev)
+    qp, shape = _on(q, _BF16, dev, "q"), q.shape
+    Bt, n_q, Hq, d2 = shape
     K = ids.shape[-1]
     if n_q != 1 or d2 != d or ids.shape != (Bt, 1, K) or page_table.dim() != 2 or \
             page_table.shape[0] != Bt:
         raise ValueError("paged attention: shapes do not match")
-    out, lse = _outputs(q, q.shape, out, lse)
-    run = _Call(ws, stream, q=q, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales,
-                v_scales=v_scales, page_table=page_table, ids=ids, out=out, lse=lse)
-    run("msa_sparse_attn_paged_i8", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-        k_scales.data_ptr(), v_scales.data_ptr(), page_table.data_ptr(), page_table.shape[1],
-        num_pages, ids.data_ptr(), out.data_ptr(), lse.data_ptr(), Bt, T, Hq, Hkv, d, block, K,
-        ws.ptr, ws.nbytes)
+    out, lse, op, lp = _outputs(q, shape, out, lse, dev)
+    _call("msa_sparse_attn_paged_i8", ws, stream, qp, *pages,
+          _on(page_table, _I32, dev, "page_table"), page_table.shape[1], num_pages,
+          _on(ids, _I32, dev, "ids"), op, lp, Bt, T, Hq, Hkv, d, block, K)
     return out, lse
 
 

@@ -84,9 +84,10 @@ typedef enum msa_status {
  * msa_sparse_attn need for these sizes (the maximum over the three; a decode
  * shape, n_q == 1, needs far less than a prefill).  The workspace must be
  * 256-byte aligned.  Its first 256 bytes hold the sticky device status word:
- * zero them once before first use (e.g. cudaMemsetAsync(ws, 0, 256)).  The
- * rest is scratch that every call overwrites; two calls that overlap in time
- * must not share a workspace.  Returns 0 for arguments the calls would reject.
+ * zero them once before first use (e.g. cudaMemsetAsync(ws, 0, 256)); the
+ * paged-cache attention calls need the whole header of
+ * MSA_WORKSPACE_HEADER_BYTES zeroed once.  The rest is scratch that every
+ * call overwrites; two calls that overlap in time must not share a workspace.  Returns 0 for arguments the calls would reject.
  *
  * Prefill attention keeps one bf16 partial (and its lse) per (query row,
  * slot, query head) until the log-sum-exp combine; it attends the kv heads in
@@ -98,6 +99,8 @@ typedef enum msa_status {
  * for kv_group kv heads per pass (kv_group = Hkv: a single pass), or 0 if
  * kv_group does not divide Hkv.
  */
+#define MSA_WORKSPACE_HEADER_BYTES 2304
+
 MSA_API size_t msa_workspace_size(int Bt, int n_q, int T, int Hq, int Hkv, int d, int d_idx,
                                   int block, int K);
 
@@ -232,8 +235,11 @@ MSA_API msa_status msa_sparse_attn_paged(const void *q, const void *k_pages, con
  * is a step without rows: MSA_OK, nothing enqueued.
  *
  * msa_cache_workspace_size: bytes of workspace for all calls of this section
- * (0 for arguments that they reject).  256-byte aligned, status word first,
- * as msa_workspace_size describes; append and gather use the status word only.
+ * (0 for arguments that they reject).  256-byte aligned, as msa_workspace_size
+ * describes: zero the first MSA_WORKSPACE_HEADER_BYTES once before first use.
+ * Behind the status word the header holds counters that every attention call
+ * leaves at zero; no other call of this library writes them.  Append and
+ * gather use the status word only.
  */
 MSA_API size_t msa_cache_workspace_size(int Hq, int Hkv, int d);
 

@@ -116,6 +116,22 @@ def attend(q, k, v, seen):
     return w @ v, lse, w @ v.abs(), size
 
 
+def fixed_point(q, k, v, seen, top_scale):
+    """Bound on what fixed-point weights add to the output's error, for int8
+    pages.  A weight w_j (relative to the largest of its row so far, hence at
+    least w_j relative to the row's largest one, w_top), times its V scale over
+    the tile's largest, is rounded to a multiple of 2^-27: the error is at most
+    half of that, and at most the weight itself where it rounds to 0.  It
+    multiplies code_j and the tile's largest scale, at most top_scale times
+    127.  For the context's rows (q [rows, d], seen [rows, keys]): [rows]."""
+    z = q @ k.t() / math.sqrt(q.shape[1])
+    z = torch.where(seen, z, torch.full_like(z, -math.inf))
+    top = z.amax(1, keepdim=True) if z.shape[1] else z.sum(1, keepdim=True)
+    w = torch.where(seen, torch.exp(z - torch.nan_to_num(top, neginf=0.0)), torch.zeros_like(z))
+    e = w.clamp(max=2.0 ** -28).sum(1) * 127 * top_scale
+    return e / w.sum(1).clamp(min=1e-300)
+
+
 def attn(x: Paged, window=0, sinks=0):
     """Reference of attn_paged over the rows 0 .. cu[-1]: out, lse, tol_out, tol_lse."""
     rows = sum(x.ns)
@@ -125,9 +141,11 @@ def attn(x: Paged, window=0, sinks=0):
     wide = torch.zeros_like(out)
     lse = torch.zeros((rows, x.Hq), dtype=torch.float64, device=dev)
     size = torch.zeros_like(lse)
+    fixed = torch.zeros_like(lse)
     at = 0
     for b, (n, t) in enumerate(zip(x.ns, x.ts)):
         k, v = x.context(b)
+        top_scale = x.vs.nan_to_num(0).max().item() if x.i8 else 0.0
         i = torch.arange(t - n, t, device=dev)[:, None]
         j = torch.arange(t, device=dev)[None]
         seen = j <= i
@@ -136,8 +154,12 @@ def attn(x: Paged, window=0, sinks=0):
         for h in range(x.Hq):
             o, l, a, s = attend(x.q[at:at + n, h].double(), k[:, h // G], v[:, h // G], seen)
             out[at:at + n, h], lse[at:at + n, h], wide[at:at + n, h], size[at:at + n, h] = o, l, a, s
+            if x.i8:
+                fixed[at:at + n, h] = fixed_point(x.q[at:at + n, h].double(), k[:, h // G],
+                                                  v[:, h // G], seen, top_scale)
         at += n
-    return out, lse, *tolerances(out, lse, wide, size, x.d)
+    t_out, t_lse = tolerances(out, lse, wide, size, x.d)
+    return out, lse, t_out + fixed[..., None], t_lse
 
 
 def tolerances(out, lse, wide, size, d):

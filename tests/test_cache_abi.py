@@ -1,7 +1,5 @@
 """Refusals of the paged-cache calls, on the host before any CUDA call, and
 the checks of their Python binding."""
-import ctypes
-
 import pytest
 import torch
 
@@ -139,17 +137,37 @@ def test_workspace_size(lib):
 
 
 def test_binding_checks():
-    """The binding refuses tensors that are not on a CUDA device, before any call."""
+    """The binding refuses tensors that are not on the workspace's device, of
+    another type or shape, or not contiguous, before any call."""
     from block_sparse_long_05_b200 import msa
+
+    class Ws:  # a workspace on a device that no tensor here is on
+        device_index = 0
+
     pages = torch.zeros((4, 32, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
-        msa.kv_append(pages[0], pages[0], pages, pages, None, None, None, None)
+        msa.kv_append(pages[0], pages[0], pages, pages, None, None, None, Ws)
     with pytest.raises(ValueError, match="CUDA"):
-        msa.attn_paged(pages[0], pages, pages, None, None, None, None)
-    with pytest.raises(ValueError, match="rows|contiguous|dimensions"):
-        msa._rows(pages[0].transpose(1, 2), "q", 3)
+        msa.attn_paged(pages[0], pages, pages, None, None, None, Ws)
+    with pytest.raises(ValueError, match="num_pages, block, Hkv, d"):
+        msa.attn_paged(pages[0], pages, pages[:3], None, None, None, Ws)
+    # (the checks themselves, with CPU tensors as if they were on the device: get_device() is -1)
+    cpu = -1
+    with pytest.raises(ValueError, match="contiguous"):
+        msa._rows(pages[0].transpose(1, 2), cpu, "q", 3)
     with pytest.raises(ValueError, match="bfloat16"):
-        msa._rows(pages[0].float(), "q", 3)
-    assert msa._rows(pages[0], "q", 3) == 128
-    assert msa._rows(pages[0, ::4], "q", 3) == 512
-    assert ctypes.sizeof(ctypes.c_int64) == 8
+        msa._rows(pages[0].float(), cpu, "q", 3)
+    with pytest.raises(ValueError, match="workspace"):
+        msa._rows(pages[0], 0, "q", 3)
+    assert msa._rows(pages[0], cpu, "q", 3) == 128
+    assert msa._rows(pages[0, ::4], cpu, "q", 3) == 512
+    scales = torch.zeros((4, 2, 32))
+    codes = pages.to(torch.int8)
+    shape, at = msa._stores(codes, codes, scales, scales, torch.int8, cpu)
+    assert shape == (4, 32, 2, 64) and len(at) == 4
+    with pytest.raises(ValueError, match="Hkv, block"):
+        msa._stores(codes, codes, scales[:, :1], scales, torch.int8, cpu)
+    i = torch.zeros((3, 5), dtype=torch.int32)
+    with pytest.raises(ValueError, match="Bt"):
+        msa._step(i, i[0, :3], i[0, :3], 4, cpu)
+    assert msa._step(i, i[0, :4], i[0, :3], 4, cpu)[0] == 3
