@@ -51,6 +51,7 @@ struct PagedAttn {
     void *out = nullptr;     // bf16 [total][Hq][d]
     float *lse = nullptr;    // fp32 [total][Hq]
     int Hq = 0, G = 0;
+    int heads = 1;           // kv heads that share a run of key tiles (divides Hkv)
     int window = 0, sinks = 0;       // window 0: every key up to the query's position
     const int32_t *ids = nullptr;    // sparse branch: [Bt][K] selected blocks (one row each)
     int K = 0, T = 0;                // sparse branch: selection width, common length
@@ -62,8 +63,9 @@ struct PagedAttn {
 };
 
 constexpr int kSplitKeys = 128;      // keys per tile of the split kernel
-constexpr int kSplitMaxRows = 32;    // query rows per tile, at most
+constexpr int kSplitMaxRows = 16;    // query rows per tile, at most
 constexpr int kSplitMaxCtas = kWsCounters;  // CTAs of the split kernel (workspace bound)
+constexpr int kSplitMaxHeads = 16;   // kv heads whose CTAs share a run of key tiles, at most
 
 // Rows of the K / V tensor map boxes of the split kernel.
 inline int split_box_rows(int block) { return block < kSplitKeys ? block : kSplitKeys; }

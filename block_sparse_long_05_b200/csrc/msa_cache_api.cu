@@ -172,6 +172,8 @@ msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int nu
     const int sms = num_sms_current();
     if (sms <= 0) return MSA_ERR_CUDA;
     const bool i8 = a.c.k_scales != nullptr;
+    for (int h = 1; h <= a.c.Hkv && h <= kSplitMaxHeads; ++h)
+        if (a.c.Hkv % h == 0) a.heads = h;
     const int box = split_box_rows(a.step.block);
     CUtensorMap tk, tv;
     if (!store_map(&tk, k_pages, num_pages, a.step.block, a.c.Hkv, a.c.d, box, i8) ||

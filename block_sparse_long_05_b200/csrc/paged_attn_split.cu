@@ -2,7 +2,7 @@
 // (single tokens, short chunks, and the sparse branch on int8 pages).
 //
 // With the rows of one (sequence, kv head) numbered r = i * G + g (token i,
-// head g of the group), a tile of R = 8, 16 or 32 rows attends its keys j with
+// head g of the group), a tile of R = 8 or 16 rows attends its keys j with
 //     s_j = (q . k_j) / sqrt(d),  m = max s_j,  l = sum exp(s_j - m),
 //     o = sum exp(s_j - m) v_j / l,  lse = m + ln l,
 // in one pass over the keys, 128 at a time, with a running m and l.
@@ -30,7 +30,10 @@
 //
 //  - The key tiles of all (sequence, row tile, kv head) segments form one
 //    list that is cut into equal runs, one per CTA: a batch with contexts of
-//    any lengths keeps every SM streaming to the end.
+//    any lengths keeps every SM streaming to the end.  Up to 16 heads share a
+//    run, each with a CTA of its own: a cached token's heads lie side by side
+//    in memory (128 bytes each with int8 and d = 128), and the CTAs that read
+//    them do it at the same time, which HBM pages and L2 lines reward.
 //  - A producer warp keeps a ring of about 100 KB (200 KB with one CTA per
 //    SM) filled by TMA, across segment borders, and looks the pages up 32
 //    tiles at a time.
@@ -53,8 +56,9 @@ namespace msa {
 namespace {
 
 constexpr int kKeys = 128;                   // keys per tile: M of the first product
-constexpr int kThreads = 128 + 32;           // warps 0-3: one key (then one value column) per
-                                             // thread; warp 4: producer
+constexpr int kCompute = 256;                // warps 0-3 and 4-7, alternate tiles: one key (then
+                                             // one value column) per thread
+constexpr int kThreads = kCompute + 64;      // warp 8: producer; warp 9: products
 constexpr int kMinRun = 2;  // tiles per run: below it the merge costs more than the run saves
 constexpr float kLn2f = 0.6931471805599453f;
 
@@ -98,7 +102,7 @@ __device__ __forceinline__ Seq seq_of(const PagedAttn &a, int b, int R) {
 }
 
 __device__ __forceinline__ long long seq_work(const PagedAttn &a, const Seq &s) {
-    return static_cast<long long>(s.nt) * a.c.Hkv * s.nk;
+    return static_cast<long long>(s.nt) * (a.c.Hkv / a.heads) * s.nk;
 }
 
 // Row tile rt of a sequence: positions of its rows and its key tiles.  Tile
@@ -132,8 +136,9 @@ __device__ __forceinline__ RowTile row_tile(const PagedAttn &a, const Seq &s, in
     return t;
 }
 
-// Where a run begins: sequence and offset in it.  All threads of the CTA take
-// part; blockDim is a multiple of 32 and at most 256.
+// Where a run begins: sequence and offset in it.  CTAs blockIdx.x / heads share
+// a run.  All threads of the CTA take
+// part; blockDim is a multiple of 32 and at most 512.
 struct Found {
     int b;
     long long off;
@@ -147,7 +152,7 @@ __device__ __forceinline__ long long run_length(long long work, int ctas) {
     return per > kMinRun ? per : kMinRun;
 }
 
-// sm: [0..7] warp sums, [8] sequence, [9] offset
+// sm: [0..15] warp sums, [16] sequence, [17] offset
 __device__ __forceinline__ Found find_run(const PagedAttn &a, int R, long long *sm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const int Bt = a.step.Bt, chunks = (Bt + blockDim.x - 1) / blockDim.x;
@@ -171,8 +176,8 @@ __device__ __forceinline__ Found find_run(const PagedAttn &a, int R, long long *
     if (lane == 0) sm[warp] = w;
     __syncthreads();
     for (int i = 0; i < nw; ++i) f.work += sm[i];
-    f.run = run_length(f.work, gridDim.x);
-    f.start = f.run * blockIdx.x;
+    f.run = run_length(f.work, gridDim.x / a.heads);
+    f.start = f.run * (blockIdx.x / a.heads);
     if (f.start >= f.work) return f;
     long long base = 0;
     for (int c = 0; c < chunks; ++c) {
@@ -193,15 +198,15 @@ __device__ __forceinline__ Found find_run(const PagedAttn &a, int R, long long *
         }
         const long long first = before + p - x;
         if (f.start >= first && f.start < first + x) {
-            sm[8] = c * static_cast<int>(blockDim.x) + threadIdx.x;
-            sm[9] = f.start - first;
+            sm[16] = c * static_cast<int>(blockDim.x) + threadIdx.x;
+            sm[17] = f.start - first;
         }
         base += all;
         if (f.start < base) break;
     }
     __syncthreads();
-    f.b = static_cast<int>(sm[8]);
-    f.off = sm[9];
+    f.b = static_cast<int>(sm[16]);
+    f.off = sm[17];
     return f;
 }
 
@@ -221,9 +226,10 @@ struct Walk {
             s = seq_of(a, b, R);
         }
         const long long seg = off / s.nk;
+        const int chunks = a.c.Hkv / a.heads;
         x0 = static_cast<int>(off - seg * s.nk);
-        rt = static_cast<int>(seg / a.c.Hkv);
-        h = static_cast<int>(seg - static_cast<long long>(rt) * a.c.Hkv);
+        rt = static_cast<int>(seg / chunks);
+        h = static_cast<int>(seg - static_cast<long long>(rt) * chunks) * a.heads + blockIdx.x % a.heads;
         const long long left = end - pos;
         x1 = left < s.nk - x0 ? x0 + static_cast<int>(left) : s.nk;
         pos += x1 - x0;
@@ -250,8 +256,10 @@ struct Tile {
     static constexpr int QBYTES = NS * D * EB;
     static constexpr int PBYTES = NO * kKeys * EB;
     // the ring takes what the 227 KB of an SM leave
-    static constexpr int STAGES = STAGE > 32768 ? 3 : STAGE > 16384 ? (R <= 8 || (!I8 && R <= 16) ? 3 : 2) : (R <= 8 ? 6 : 5);
-    static constexpr int TMEM = NS + NO <= 32 ? 32 : NS + NO <= 64 ? 64 : NS + NO <= 128 ? 128 : 256;
+    static constexpr int STAGES = STAGE > 32768 ? 3 : STAGE > 16384 ? (R <= 8 ? 3 : 2) : 5;
+    static constexpr int COLS = 2 * (NS + NO);  // both warpgroups
+    static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
+    static_assert(COLS <= 256, "two CTAs share the 512 columns of an SM");
 };
 
 struct alignas(16) StageMeta {
@@ -259,13 +267,14 @@ struct alignas(16) StageMeta {
 };
 
 constexpr int kScaleBytes = 2 * kKeys * 4;  // K and V scales of a stage
-constexpr int kMergeFloats = 1024;          // weights of a chunk of pieces (in the buffer of P)
+constexpr int kMergeFloats = 1024;          // weights of a chunk of pieces, 8 rows at a time
+                                            // (in the buffer of P)
 
 template <int D, bool I8, int R>
 constexpr size_t split_smem_bytes() {
     using T = Tile<D, I8, R>;
     return 1024 + static_cast<size_t>(T::STAGES) * T::STAGE + round_up(T::QBYTES, 1024) +
-           round_up(T::PBYTES, 1024) + (I8 ? T::STAGES * kScaleBytes : 0) + (R + 1) * 16 + R * 20 + 16 + T::STAGES * (sizeof(StageMeta) + 16) + 128;
+           2 * round_up(T::PBYTES, 1024) + (I8 ? T::STAGES * kScaleBytes : 0) + 2 * (R + 4) * 16 + R * 36 + 16 + T::STAGES * (sizeof(StageMeta) + 16) + 216;
 }
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -283,11 +292,10 @@ __device__ __forceinline__ float warp_max(float x) {
     return r;
 }
 
-// 8 columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                   "=r"(r[7])
+// 4 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(taddr)
                  : "memory");
 }
@@ -324,99 +332,84 @@ constexpr uint32_t kIdescAMn = 1u << 15;  // A runs along M in memory
 // ===========================================================================
 // Merge of the pieces of a segment whose first run is c0 and last run c1:
 //   lse = log2 sum 2^lse_p,  out = sum 2^(lse_p - lse) o_p
-// by the 128 threads of warps 0-3, a value column each.  wt: kMergeFloats.
+// by the compute threads: a value column and half of the rows each.
+// wt: kMergeFloats weights, tops: [R] maxima.
 // ===========================================================================
 template <int D, int R>
 __device__ __noinline__ void merge_pieces(const PagedAttn &a, const RowTile &t, int cu0, int h, int c0,
-                                          int c1, bool first, float *wt) {
-    constexpr int RG = 8;                      // rows at a time
-    constexpr int CH = kMergeFloats / RG - 1;  // pieces per chunk; the last row holds the maxima
-    const int tid = threadIdx.x, pieces = c1 - c0 + 1, col = tid < D ? tid : 0;
+                                          int c1, bool first, float *wt, float *tops) {
+    constexpr int CH = kMergeFloats / 8;  // pieces per chunk
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int pieces = c1 - c0 + 1, live = min(t.rows - t.r0, R);
     // the first run's piece is its last one, unless the run begins with it
-    auto slot = [&](int p) { return 2ll * (c0 + p) + (p == 0 && !first ? 1 : 0); };
+    auto slot = [&](int p) { return 2ll * ((c0 + p) * a.heads + blockIdx.x % a.heads) + (p == 0 && !first ? 1 : 0); };
+    // a warp finds the maximum of a row over all pieces
+    for (int r = warp; r < live; r += kCompute / 32) {
+        float g = -INFINITY;
+        for (int p = lane; p < pieces; p += 32) g = fmaxf(g, __ldcg(a.part_lse + slot(p) * R + r));
+        g = warp_max(g);
+        if (lane == 0) tops[r] = g;
+    }
+    named_barrier(1, kCompute);
+    constexpr int RH = 4;  // rows of a thread at a time
+    const int col = (tid & 127) < D ? tid & 127 : 0;
 #pragma unroll 1
-    for (int rg = 0; rg < min(t.rows - t.r0, R); rg += RG) {
-        const int live = min(t.rows - t.r0, R) - rg;
-        float acc[RG], sum[RG], top[RG];
+    for (int rg = 0; rg < live; rg += 2 * RH) {
+        const int r0 = rg + (tid >> 7) * RH;  // (the two halves of the threads)
+        float acc[RH], sum[RH];
 #pragma unroll
-        for (int r = 0; r < RG; ++r) {
-            acc[r] = sum[r] = 0.f;
-            top[r] = -INFINITY;
-        }
+        for (int r = 0; r < RH; ++r) acc[r] = sum[r] = 0.f;
 #pragma unroll 1
         for (int p0 = 0; p0 < pieces; p0 += CH) {
             const int m = min(CH, pieces - p0);
-            named_barrier(1, 128);
-            for (int e = tid; e < m * RG; e += 128)
-                wt[e] = e % RG < live ? __ldcg(a.part_lse + slot(p0 + e / RG) * R + rg + e % RG) : -INFINITY;
-            named_barrier(1, 128);
-            if (tid < RG) {
-                float g = -INFINITY;
-                for (int p = 0; p < m; ++p) g = fmaxf(g, wt[p * RG + tid]);
-                wt[CH * RG + tid] = g;
+            for (int e = tid; e < m * 2 * RH; e += kCompute) {
+                const int r = rg + e % (2 * RH);
+                float w = 0.f;  // 0: the piece has no key of the row
+                if (r < live) {
+                    const float l = __ldcg(a.part_lse + slot(p0 + e / (2 * RH)) * R + r), g = tops[r];
+                    // (a weight that underflows stays above 0, for the sake of a NaN)
+                    if (l != -INFINITY) {
+                        w = ex2_approx(l - (g == -INFINITY ? 0.f : g));
+                        if (w == 0.f) w = 1.2e-38f;
+                    }
+                }
+                wt[e] = w;
             }
-            named_barrier(1, 128);
-            float f[RG];
-#pragma unroll
-            for (int r = 0; r < RG; ++r) {
-                const float g = fmaxf(top[r], wt[CH * RG + r]);
-                f[r] = top[r] == -INFINITY ? 0.f : ex2_approx(top[r] - g);
-                top[r] = g;
-            }
-            for (int e = tid; e < m * RG; e += 128) {
-                const float l = wt[e], g = fmaxf(wt[CH * RG + e % RG], -3e38f);
-                // relative to this chunk's maximum; 0: the piece has no key of the row
-                // (a weight that underflows stays above 0, for the sake of a NaN)
-                const float w = ex2_approx(l - g);
-                wt[e] = l == -INFINITY ? 0.f : w == 0.f ? 1.2e-38f : w;
-            }
-            named_barrier(1, 128);
-#pragma unroll
-            for (int r = 0; r < RG; ++r) {
-                acc[r] *= f[r];
-                sum[r] *= f[r];
-            }
-            float part[RG], psum[RG];
-#pragma unroll
-            for (int r = 0; r < RG; ++r) part[r] = psum[r] = 0.f;
+            named_barrier(1, kCompute);
 #pragma unroll 1
             for (int p = 0; p < m; p += 4) {
-                float y[4][RG];
+                float y[4][RH];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int r = 0; r < RG; ++r)
-                        y[k][r] = p + k < m && r < live ? __ldcg(a.part_o + (slot(p0 + p + k) * R + rg + r) * D + col) : 0.f;
+                    for (int r = 0; r < RH; ++r)
+                        y[k][r] = p + k < m && r0 + r < live ? __ldcg(a.part_o + (slot(p0 + p + k) * R + r0 + r) * D + col) : 0.f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if (p + k >= m) break;
+                    const float4 w4 = *reinterpret_cast<const float4 *>(wt + (p + k) * 2 * RH + (tid >> 7) * RH);
+                    const float w[RH] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                    for (int r = 0; r < RG; ++r) {
-                        const float w = wt[(p + k) * RG + r];
-                        psum[r] += w;
-                        part[r] += w == 0.f ? 0.f : w * y[k][r];
+                    for (int r = 0; r < RH; ++r) {
+                        sum[r] += w[r];
+                        acc[r] += w[r] == 0.f ? 0.f : w[r] * y[k][r];
                     }
                 }
             }
-#pragma unroll
-            for (int r = 0; r < RG; ++r) {
-                const float g = wt[CH * RG + r];
-                const float w = g == -INFINITY ? (psum[r] == psum[r] ? 0.f : 1.f) : ex2_approx(g - top[r]);
-                acc[r] += w * part[r];
-                sum[r] += w * psum[r];
-            }
+            named_barrier(1, kCompute);
         }
 #pragma unroll
-        for (int r = 0; r < RG; ++r) {
-            if (r >= live || tid >= D) continue;
-            const int row = t.r0 + rg + r, tok = row / a.G;
+        for (int r = 0; r < RH; ++r) {
+            if (r0 + r >= live || (tid & 127) >= D) continue;
+            const int row = t.r0 + r0 + r, tok = row / a.G;
             const long long orow = (static_cast<long long>(cu0) + tok) * a.Hq + static_cast<long long>(h) * a.G + (row - tok * a.G);
-            const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
-            static_cast<__nv_bfloat16 *>(a.out)[orow * D + tid] = __float2bfloat16_rn(acc[r] * inv);
-            if (tid == 0) a.lse[orow] = sum[r] == 0.f ? -INFINITY : (top[r] + __log2f(sum[r])) * kLn2f;
+            const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r], g = tops[r0 + r];
+            static_cast<__nv_bfloat16 *>(a.out)[orow * D + (tid & 127)] = __float2bfloat16_rn(acc[r] * inv);
+            if ((tid & 127) == 0)
+                a.lse[orow] = sum[r] == 0.f ? -INFINITY : ((g == -INFINITY ? 0.f : g) + __log2f(sum[r])) * kLn2f;
         }
-        named_barrier(1, 128);
     }
+    named_barrier(1, kCompute);
 }
 
 // ===========================================================================
@@ -432,20 +425,25 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *q_s = ring + T::STAGES * T::STAGE;
     unsigned char *p_s = q_s + round_up(T::QBYTES, 1024);
-    float *scales = reinterpret_cast<float *>(p_s + round_up(T::PBYTES, 1024));  // [stage][K, V][128]
+    float *scales = reinterpret_cast<float *>(p_s + 2 * round_up(T::PBYTES, 1024));  // [stage][K, V][128]
     static_assert(T::PBYTES >= kMergeFloats * 4, "merge weights");
-    float4 *tops = reinterpret_cast<float4 *>(scales + (I8 ? T::STAGES * 2 * kKeys : 0));  // [row] maxima of the 4 warps; [R]: of sv
-    float *qscale = reinterpret_cast<float *>(tops + R + 1);       // [R] factor of a row's scores
-    float *maxima = qscale + R;                                    // [2][R] the rows' m, tile about
-    int *rowpos = reinterpret_cast<int *>(maxima + 2 * R);         // [R] position, -1: no such row
+    constexpr int TW = R + 4;  // maxima of a warp: its rows' scores, then its V scales
+    float *tops_s = scales + (I8 ? T::STAGES * 2 * kKeys : 0);     // [warp][TW]
+    float *qscale = tops_s + 8 * TW;                               // [R] factor of a row's scores
+    float *maxima_s = qscale + R;                                  // [warpgroup][2][R] the rows' m, tile about
+    float *sums = maxima_s + 4 * R;                                // [warpgroup][R] the rows' l
+    int *rowpos = reinterpret_cast<int *>(sums + 2 * R);           // [R] position, -1: no such row
     int *poison = rowpos + R;                                      // [R] a seen key's sv is not finite
     StageMeta *meta = reinterpret_cast<StageMeta *>(
         (reinterpret_cast<uintptr_t>(poison + R) + 15) & ~static_cast<uintptr_t>(15));
     uint64_t *full = reinterpret_cast<uint64_t *>(meta + T::STAGES);
     uint64_t *empty = full + T::STAGES;
-    uint64_t *bar_s = empty + T::STAGES, *bar_o = bar_s + 1;
-    long long *scan = reinterpret_cast<long long *>(bar_o + 1);  // [10]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(scan + 10);
+    uint64_t *bar_s = empty + T::STAGES;  // [warpgroup] scores complete
+    uint64_t *bar_o = bar_s + 2;          // [warpgroup] outputs complete
+    uint64_t *p_ready = bar_s + 4;        // [warpgroup] weights written, scores and last outputs read
+    uint64_t *q_ready = bar_s + 6;        // Q of a segment written
+    long long *scan = reinterpret_cast<long long *>(bar_s + 7);  // [18]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(scan + 18);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *last_piece = abort_flag + 1;
 
@@ -455,19 +453,34 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
             mbar_init(full + i, 1);
             mbar_init(empty + i, 1);
         }
-        mbar_init(bar_s, 1);
-        mbar_init(bar_o, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_s + i, 1);
+            mbar_init(bar_o + i, 1);
+            mbar_init(p_ready + i, kCompute / 2);
+        }
+        mbar_init(q_ready, kCompute);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    const Found found = find_run(a, R, scan);
+    if (tid < kCompute) {  // rows of the operand buffer that no digit or head ever fills
+        for (int e = tid; e < T::QBYTES / 16; e += kCompute) reinterpret_cast<uint4 *>(q_s)[e] = make_uint4(0, 0, 0, 0);
+    }
+    const Found found = find_run(a, R, scan);  // (its barriers order the writes above)
     if (found.start >= found.work) return;
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, T::TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;  // per warpgroup: NS columns of scores, NO of outputs
     Walk walk(found);
     const int block = a.step.block;
 
-    if (warp == 4) {
+    if (warp == 8) {
         // -------------------------------------------------------- producer
         uint32_t it = 0;
         const int box = min(block, kKeys);  // keys per TMA box
@@ -565,23 +578,73 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
         return;
     }
 
-    // ------------------------------------------------------------ warps 0-3
-    if (warp == 0) {
-        tmem_alloc(tmem_slot, T::TMEM);
-        tmem_relinquish();
+    if (warp == 9) {
+        // -------------------------------------------------------- products
+        // Tiles alternate between the warpgroups.  S^T of a tile is issued as soon
+        // as its keys have landed, before the O^T of the tile before, whose
+        // weights the other warpgroup is still at.
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = I8 ? idesc_s8_s32(128, T::NS) : idesc_bf16_f32(128, T::NS, false);
+            constexpr uint32_t idesc_o = (I8 ? idesc_s8_s32(128, T::NO) : idesc_bf16_f32(128, T::NO, false)) | kIdescAMn;
+            constexpr int EK = I8 ? 32 : 16;  // contraction of one instruction (32 bytes)
+            const uint64_t kd0 = row_desc<T::ROWB>(smem_addr(ring + T::BYTES)), qd0 = row_desc<T::ROWB>(smem_addr(q_s));
+            const uint64_t vd0 = col_desc<T::ROWB, T::REGION>(smem_addr(ring)), pd0 = row_desc<128>(smem_addr(p_s));
+            uint32_t it = 0, segs = 0;
+            bool ok = true;
+            auto outputs = [&](uint32_t i) {  // O^T of tile i
+                const uint32_t g = i & 1;
+                if (!(ok = mbar_wait(p_ready + g, i >> 1 & 1, abort_flag, a.status))) return;
+                tc_fence_after();
+                const uint32_t st = i % T::STAGES, tmem_o = tmem + g * (T::NS + T::NO) + T::NS;
+#pragma unroll
+                for (int k = 0; k < kKeys / EK; ++k) {
+                    const uint64_t vd = vd0 + st * (T::STAGE >> 4) + ((k * EK * T::ROWB) >> 4);
+                    const uint64_t pd = pd0 + ((g * round_up(T::PBYTES, 1024) + (k / 4) * T::NO * 128 + (k % 4) * 32) >> 4);
+                    if (I8)
+                        umma_i8(tmem_o, vd, pd, idesc_o, k > 0);
+                    else
+                        umma_bf16(tmem_o, vd, pd, idesc_o, k > 0);
+                }
+                umma_commit(bar_o + g);
+                umma_commit(empty + st);
+            };
+            while (ok && walk.next(a, R)) {
+                const RowTile t = row_tile(a, walk.s, walk.rt, R);
+                const int x1 = min(walk.x1, t.count);
+                ok = mbar_wait(q_ready, segs++ & 1, abort_flag, a.status);
+                for (int x = walk.x0; x < x1 && ok; ++x, ++it) {
+                    const uint32_t st = it % T::STAGES, tmem_s = tmem + (it & 1) * (T::NS + T::NO);
+                    if (!(ok = mbar_wait(full + st, (it / T::STAGES) & 1, abort_flag, a.status))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < D / EK; ++k) {
+                        const uint64_t kd = kd0 + st * (T::STAGE >> 4) + (((k / 4) * T::REGION + (k % 4) * 32) >> 4);
+                        const uint64_t qd = qd0 + (((k / 4) * T::NS * 128 + (k % 4) * 32) >> 4);
+                        if (I8)
+                            umma_i8(tmem_s, kd, qd, idesc_s, k > 0);
+                        else
+                            umma_bf16(tmem_s, kd, qd, idesc_s, k > 0);
+                    }
+                    umma_commit(bar_s + (it & 1));
+                    if (x > walk.x0) outputs(it - 1);
+                }
+                if (ok && x1 > walk.x0) outputs(it - 1);
+            }
+        }
+        __syncwarp();
+        named_barrier(2, kCompute + 32);  // the compute warps have read their last outputs
+        tmem_dealloc(tmem, T::TMEM);
+        return;
     }
-    // rows of the operand buffers that no digit or head ever fills
-    for (int e = tid; e < T::QBYTES / 16; e += 128) reinterpret_cast<uint4 *>(q_s)[e] = make_uint4(0, 0, 0, 0);
-    tc_fence_before();
-    named_barrier(1, 128);
-    tc_fence_after();
-    const uint32_t tmem_s = *tmem_slot, tmem_o = tmem_s + T::NS;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    constexpr uint32_t idesc_s = I8 ? idesc_s8_s32(128, T::NS) : idesc_bf16_f32(128, T::NS, false);
-    constexpr uint32_t idesc_o = (I8 ? idesc_s8_s32(128, T::NO) : idesc_bf16_f32(128, T::NO, false)) | kIdescAMn;
-    constexpr int EK = I8 ? 32 : 16;  // contraction of one instruction (32 bytes)
 
-    uint32_t it = 0, n_s = 0;  // tiles taken; products of each kind awaited
+    // ------------------------------------------------------------ warps 0-7
+    const uint32_t wg = warp >> 2;  // warpgroup
+    const int key = tid & 127, quarter = warp & 3;
+    const uint32_t tmem_s = tmem + wg * (T::NS + T::NO) + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t tmem_o = tmem_s + T::NS;
+    unsigned char *p_w = p_s + wg * round_up(T::PBYTES, 1024);
+    float *tops = tops_s + wg * 4 * TW, *maxima = maxima_s + wg * 2 * R;
+    uint32_t it = 0;           // tiles taken (by both warpgroups)
     bool ok = true;            // false: a wait of this thread gave up
     bool dead = false;         // the same for all: no tile is taken any more, but every
                                // barrier is met
@@ -592,9 +655,9 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
         // ---- Q rows into shared memory, 16 threads per row (8 with d = 64)
         constexpr int TPR = D / 8;
 #pragma unroll
-        for (int rr = 0; rr < R; rr += 128 / TPR) {
+        for (int rr = 0; rr < R; rr += kCompute / TPR) {
             const int r = rr + tid / TPR, c = tid % TPR;
-            if (R % (128 / TPR) != 0 && r >= R) continue;  // (whole warps)
+            if (R % (kCompute / TPR) != 0 && r >= R) continue;  // (whole warps)
             const int row = t.r0 + r, tok = row / a.G;
             uint4 u = make_uint4(0, 0, 0, 0);
             if (row < t.rows)
@@ -603,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                     (static_cast<long long>(walk.h) * a.G + (row - tok * a.G)) * D + c * 8);
             if (c == 0) {
                 rowpos[r] = row < t.rows ? walk.s.off + tok : -1;
-                maxima[r] = -INFINITY;
+                maxima_s[r] = maxima_s[2 * R + r] = -INFINITY;
                 if (I8) poison[r] = 0;
             }
             if (!I8) {
@@ -644,7 +707,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
             }
         }
         fence_proxy_async_smem();
-        named_barrier(1, 128);
+        mbar_arrive(q_ready);
+        named_barrier(1, kCompute);  // rowpos, qscale, maxima
 
         float o[R], l[R];  // this column's sums, this key lane's weights
 #pragma unroll
@@ -652,60 +716,54 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
         const float *m = maxima;  // the rows' running maxima
         const int last = min(t.tmax, walk.s.cap - 1);  // last key that any row sees
 
-        for (int x = walk.x0; x < x1 && !dead; ++x) {
-            const int st = it % T::STAGES;
-            ok = ok && mbar_wait(full + st, (it / T::STAGES) & 1, abort_flag, a.status);
-            unsigned char *vs = ring + st * T::STAGE, *ks = vs + T::BYTES;
-            if (tid == 0 && ok) {
-                tc_fence_after();
-                const uint32_t ka = smem_addr(ks), qa = smem_addr(q_s);
-#pragma unroll
-                for (int k = 0; k < D / EK; ++k) {
-                    const uint64_t kd = row_desc<T::ROWB>(ka + (k / 4) * T::REGION + (k % 4) * 32);
-                    const uint64_t qd = row_desc<T::ROWB>(qa + (k / 4) * T::NS * 128 + (k % 4) * 32);
-                    if (I8)
-                        umma_i8(tmem_s, kd, qd, idesc_s, k > 0);
-                    else
-                        umma_bf16(tmem_s, kd, qd, idesc_s, k > 0);
-                }
-                umma_commit(bar_s);
-            }
-            // this thread's key
-            const int base = ok ? meta[st].pos[warp] : -1;
-            const int pos = base < 0 ? 0x7FFFFFFF : base + lane;
-            const bool any = pos <= last && (!a.window || pos > t.tmin - a.window || pos < a.sinks);
-            const bool every = pos <= min(t.tmin, walk.s.cap - 1) && (!a.window || pos > t.tmax - a.window || pos < a.sinks);
-            float sk = 1.f, sv = 1.f;
-            bool bad_sv = false;
+        // This thread's key of a tile: its position, whether any row or every row
+        // sees it, its scales; read one tile ahead, while the products run.
+        int pos = 0;
+        bool any = false, every = false, bad_sv = false;
+        float sk = 1.f, sv = 1.f;
+        auto take_key = [&](uint32_t i) {
+            const int st = i % T::STAGES;
+            ok = ok && mbar_wait(full + st, (i / T::STAGES) & 1, abort_flag, a.status);
+            const int base = ok ? meta[st].pos[quarter] : -1;
+            pos = base < 0 ? 0x7FFFFFFF : base + lane;
+            any = pos <= last && (!a.window || pos > t.tmin - a.window || pos < a.sinks);
+            every = pos <= min(t.tmin, walk.s.cap - 1) && (!a.window || pos > t.tmax - a.window || pos < a.sinks);
             if (I8) {
-                sk = scales[2 * st * kKeys + tid];
-                sv = any ? scales[(2 * st + 1) * kKeys + tid] : 0.f;
+                sk = scales[2 * st * kKeys + key];
+                sv = any ? scales[(2 * st + 1) * kKeys + key] : 0.f;
                 bad_sv = !(sv <= 3.4028235e38f);  // inf or NaN
                 if (bad_sv) sv = 0.f;
                 const float top = warp_max(sv);
-                if (lane == 0) reinterpret_cast<float *>(tops + R)[warp] = top;
+                if (lane == 0) tops[quarter * TW + R + (i >> 1 & 1)] = top;
             } else if (!any) {
                 // a key that no row sees counts nothing, whatever its V row holds
 #pragma unroll
-                for (int r = 0; r < T::REGS; ++r)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4 *>(vs + r * T::REGION + tid * 128 + ((c + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < 8 * T::REGS; ++c)
+                    *reinterpret_cast<uint4 *>(ring + st * T::STAGE + c / 8 * T::REGION + key * 128 + ((c + lane) & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
             }
+        };
+        const uint32_t end = it + max(x1 - walk.x0, 0);  // tiles taken after this segment
+        uint32_t i = it + ((it ^ wg) & 1);               // the warpgroup's first tile of it
+        if (i < end && !dead) take_key(i);
+        for (; i < end && !dead; i += 2) {
             const bool all = __all_sync(0xFFFFFFFFu, every);
-            ok = ok && mbar_wait(bar_s, n_s & 1, abort_flag, a.status);
+            ok = ok && mbar_wait(bar_s + wg, i >> 1 & 1, abort_flag, a.status);
             tc_fence_after();
             float s[R];
 #pragma unroll
-            for (int r0 = 0; r0 < R; r0 += 8) {
-                uint32_t w[I8 ? 3 : 1][8];
+            for (int r0 = 0; r0 < R; r0 += 4) {
+                uint32_t w[I8 ? 3 : 1][4];
 #pragma unroll
-                for (int i = 0; i < (I8 ? 3 : 1); ++i) tmem_ld8(tmem_s + lanes + i * R + r0, w[i]);
+                for (int k = 0; k < (I8 ? 3 : 1); ++k) tmem_ld4(tmem_s + k * R + r0, w[k]);
+                float4 qs = make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2);
+                if (I8) qs = *reinterpret_cast<const float4 *>(qscale + r0);
+                const float f[4] = {qs.x, qs.y, qs.z, qs.w};
                 tmem_wait_ld();
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    s[r0 + r] = I8 ? from_digits(w[0][r], w[I8][r], w[2 * I8][r]) * (qscale[r0 + r] * sk)
-                                   : __uint_as_float(w[0][r]) * a.scale_log2;
+                for (int r = 0; r < 4; ++r)
+                    s[r0 + r] = I8 ? from_digits(w[0][r], w[I8][r], w[2 * I8][r]) * (f[r] * sk)
+                                   : __uint_as_float(w[0][r]) * f[r];
             }
             if (!all) {
 #pragma unroll
@@ -720,112 +778,132 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                 for (int r = 0; r < R; ++r) poison[r] = 1;
             }
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float g = warp_max(s[r]);
-                if (lane == 0) reinterpret_cast<float *>(tops + r)[warp] = g;
+            for (int r = 0; r < R; r += 4) {
+                const float4 g = make_float4(warp_max(s[r]), warp_max(s[r + 1]), warp_max(s[r + 2]), warp_max(s[r + 3]));
+                if (lane == 0) *reinterpret_cast<float4 *>(tops + quarter * TW + r) = g;
             }
-            tc_fence_before();
-            dead = named_barrier_or(1, 128, !ok);
+            dead = named_barrier_or(3 + wg, 128, !ok);
             if (dead) break;
             // ---- weights, relative to the running maxima
-            float svmax = 1.f, svr = 1.f;
+            float svmax = 1.f, unit_sv = 1.f;
             if (I8) {
-                const float4 g = tops[R];
-                svmax = fmaxf(fmaxf(g.x, g.y), fmaxf(g.z, g.w));
-                svr = svmax > 1e-37f ? sv * __frcp_rn(svmax) : 0.f;
+                const float *g = tops + R + (i >> 1 & 1);
+                svmax = fmaxf(fmaxf(g[0], g[TW]), fmaxf(g[2 * TW], g[3 * TW]));
+                unit_sv = svmax > 1e-37f ? sv * __frcp_rn(svmax) * 134217728.f : 0.f;  // 2^27 sv / svmax
             }
             float *mnext = maxima + (m == maxima ? R : 0);
+            if (key < R)
+                mnext[key] = fmaxf(fmaxf(fmaxf(tops[key], tops[TW + key]), fmaxf(tops[2 * TW + key], tops[3 * TW + key])), m[key]);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float4 g = tops[r];
-                const float mo = m[r], mn = fmaxf(fmaxf(fmaxf(g.x, g.y), fmaxf(g.z, g.w)), mo);
-                if (mn != mo) {  // (the same for all threads)
-                    const float f = mo == -INFINITY ? (l[r] == 0.f ? 0.f : 1.f) : ex2_approx(mo - mn);
-                    o[r] *= f;
-                    l[r] *= f;
+            for (int r0 = 0; r0 < R; r0 += 4) {
+                float mo[4], mn[4];
+                *reinterpret_cast<float4 *>(mo) = *reinterpret_cast<const float4 *>(m + r0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mn[e] = mo[e];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float4 g = *reinterpret_cast<const float4 *>(tops + w * TW + r0);
+                    mn[0] = fmaxf(mn[0], g.x);
+                    mn[1] = fmaxf(mn[1], g.y);
+                    mn[2] = fmaxf(mn[2], g.z);
+                    mn[3] = fmaxf(mn[3], g.w);
                 }
-                if (tid == 0) mnext[r] = mn;
-                const float p = ex2_approx(s[r] - (mn == -INFINITY ? 0.f : mn));
-                l[r] += p;
-                if (I8) {
-                    const uint32_t y = __float2uint_rn(p * svr * 134217728.f);  // 2^27, at most
+                if (mn[0] != mo[0] || mn[1] != mo[1] || mn[2] != mo[2] || mn[3] != mo[3]) {  // (the same for all)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        p_s[sw128_offset(i * R + r, tid / 16) + tid % 16] = static_cast<unsigned char>(y >> (7 * i) & 0x7Fu);
-                } else {
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(p), lo = __float2bfloat16_rn(p - __bfloat162float(hi));
-                    unsigned char *at = p_s + (tid / 64) * T::NO * 128 + tid % 8 * 2;
-                    *reinterpret_cast<__nv_bfloat16 *>(at + sw128_offset(r, tid % 64 / 8)) = hi;
-                    *reinterpret_cast<__nv_bfloat16 *>(at + sw128_offset(R + r, tid % 64 / 8)) = lo;
+                    for (int e = 0; e < 4; ++e) {
+                        const float f = mo[e] == -INFINITY ? (l[r0 + e] == 0.f ? 0.f : 1.f) : ex2_approx(mo[e] - mn[e]);
+                        o[r0 + e] *= f;
+                        l[r0 + e] *= f;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = r0 + e;
+                    const float p = ex2_approx(s[r0 + e] - (mn[e] == -INFINITY ? 0.f : mn[e]));
+                    l[r0 + e] += p;
+                    if (I8) {
+                        const uint32_t y = __float2uint_rn(p * unit_sv);  // 2^27, at most
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            p_w[sw128_offset(k * R + r, key / 16) + key % 16] = static_cast<unsigned char>(y >> (7 * k) & 0x7Fu);
+                    } else {
+                        const __nv_bfloat16 hi = __float2bfloat16_rn(p), lo = __float2bfloat16_rn(p - __bfloat162float(hi));
+                        unsigned char *at = p_w + (key / 64) * T::NO * 128 + key % 8 * 2;
+                        *reinterpret_cast<__nv_bfloat16 *>(at + sw128_offset(r, key % 64 / 8)) = hi;
+                        *reinterpret_cast<__nv_bfloat16 *>(at + sw128_offset(R + r, key % 64 / 8)) = lo;
+                    }
                 }
             }
             m = mnext;
             fence_proxy_async_smem();
-            named_barrier(1, 128);
-            if (tid == 0) {
-                tc_fence_after();
-                const uint32_t va = smem_addr(vs), pa = smem_addr(p_s);
-#pragma unroll
-                for (int k = 0; k < kKeys / EK; ++k) {
-                    const uint64_t vd = col_desc<T::ROWB, T::REGION>(va + k * EK * T::ROWB);
-                    const uint64_t pd = row_desc<128>(pa + (k / 4) * T::NO * 128 + (k % 4) * 32);
-                    if (I8)
-                        umma_i8(tmem_o, vd, pd, idesc_o, k > 0);
-                    else
-                        umma_bf16(tmem_o, vd, pd, idesc_o, k > 0);
-                }
-                umma_commit(bar_o);
-            }
-            ok = mbar_wait(bar_o, n_s & 1, abort_flag, a.status);  // (ok: the barrier saw it)
-            ++n_s;
+            tc_fence_before();
+            mbar_arrive(p_ready + wg);
+            if (i + 2 < end) take_key(i + 2);
+            ok = mbar_wait(bar_o + wg, i >> 1 & 1, abort_flag, a.status) && ok;
             tc_fence_after();
             const float unit = svmax * 7.450580596923828e-9f;  // 2^-27
 #pragma unroll
-            for (int r0 = 0; r0 < R; r0 += 8) {
-                uint32_t w[I8 ? 4 : 2][8];
+            for (int r0 = 0; r0 < R; r0 += 4) {
+                uint32_t w[I8 ? 4 : 2][4];
 #pragma unroll
-                for (int i = 0; i < (I8 ? 4 : 2); ++i) tmem_ld8(tmem_o + lanes + i * R + r0, w[i]);
+                for (int k = 0; k < (I8 ? 4 : 2); ++k) tmem_ld4(tmem_o + k * R + r0, w[k]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
+                for (int r = 0; r < 4; ++r)
                     o[r0 + r] = I8 ? fmaf(from_digits(w[0][r], w[1][r], w[2 * I8][r] + 128 * w[3 * I8][r]), unit, o[r0 + r])
                                    : o[r0 + r] + (__uint_as_float(w[0][r]) + __uint_as_float(w[1][r]));
             }
-            tc_fence_before();
-            if (tid == 0) mbar_arrive(empty + st);  // (thread 0 saw both products complete)
-            ++it;
         }
+        it = end;
 
-        // ---- end of the segment: the rows' sums over the 128 key lanes
-        named_barrier(1, 128);  // (the last tile's reads of tops are done)
+        // ---- end of the segment: the rows' sums over the key lanes, then both
+        // warpgroups' results (merge buffer: the weights', which are all read)
+        named_barrier(1, kCompute);  // (both have their last outputs)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float y = l[r];
 #pragma unroll
             for (int k = 16; k; k >>= 1) y += __shfl_xor_sync(0xFFFFFFFFu, y, k);
-            if (lane == 0) reinterpret_cast<float *>(tops + r)[warp] = y;
+            if (lane == 0) tops[quarter * TW + r] = y;
         }
-        named_barrier(1, 128);
+        named_barrier(3 + wg, 128);
+        if (key < R) {
+            sums[wg * R + key] = (tops[key] + tops[TW + key]) + (tops[2 * TW + key] + tops[3 * TW + key]);
+            if (m != maxima) maxima[key] = maxima[R + key];
+        }
+        // the second warpgroup hands over its columns' sums; it then writes the
+        // second half of the rows
+        float *pool = reinterpret_cast<float *>(p_s);
+        static_assert(2 * T::PBYTES >= R * 128 * 4, "exchange buffer");
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r) pool[(r + wg * (R / 2)) * 128 + key] = wg ? o[r] : o[R / 2 + r];
+        named_barrier(1, kCompute);
         const bool lead = walk.pos - (walk.x1 - walk.x0) == found.start;  // the run's first piece
         const long long prow = (2ll * blockIdx.x + (lead ? 0 : 1)) * R;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int row = t.r0 + r;
+        for (int e = 0; e < R / 2; ++e) {
+            const int r = wg * (R / 2) + e, row = t.r0 + r;
             if (row >= t.rows) break;
-            const float4 y = tops[r];
-            const float sum = (y.x + y.y) + (y.z + y.w);
+            const float mine = wg ? o[R / 2 + e] : o[e], other = pool[(e + (wg ^ 1) * (R / 2)) * 128 + key];
+            const float m0 = maxima_s[wg * 2 * R + r], m1 = maxima_s[(wg ^ 1) * 2 * R + r];
+            const float l0 = sums[wg * R + r], l1 = sums[(wg ^ 1) * R + r];
+            const float top = fmaxf(m0, m1);
+            const float f0 = m0 == -INFINITY ? (l0 == 0.f ? 0.f : 1.f) : ex2_approx(m0 - top);
+            const float f1 = m1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : ex2_approx(m1 - top);
+            const float sum = l0 * f0 + l1 * f1;
             float inv = sum == 0.f ? 0.f : 1.f / sum;
             if (I8 && poison[r]) inv = __uint_as_float(0x7FC00000u);
-            const float lse2 = sum == 0.f ? -INFINITY : (m[r] == -INFINITY ? 0.f : m[r]) + __log2f(sum);
+            const float y = (mine * f0 + other * f1) * inv;
+            const float lse2 = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) + __log2f(sum);
             if (whole) {
                 const int tok = row / a.G;
                 const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq +
                                        static_cast<long long>(walk.h) * a.G + (row - tok * a.G);
-                if (tid < D) static_cast<__nv_bfloat16 *>(a.out)[orow * D + tid] = __float2bfloat16_rn(o[r] * inv);
-                if (tid == 0) a.lse[orow] = lse2 * kLn2f;
+                if (key < D) static_cast<__nv_bfloat16 *>(a.out)[orow * D + key] = __float2bfloat16_rn(y);
+                if (key == 0) a.lse[orow] = lse2 * kLn2f;
             } else {
-                if (tid < D) a.part_o[(prow + r) * D + tid] = o[r] * inv;
-                if (tid == 0) a.part_lse[prow + r] = lse2;
+                if (key < D) a.part_o[(prow + r) * D + key] = y;
+                if (key == 0) a.part_lse[prow + r] = lse2;
             }
         }
         if (!whole) {
@@ -833,21 +911,22 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
             const long long seg0 = walk.pos - walk.x1, seg1 = seg0 + walk.s.nk;
             const int c0 = static_cast<int>(seg0 / found.run), c1 = static_cast<int>((seg1 - 1) / found.run);
             __threadfence();
-            named_barrier(1, 128);
-            if (tid == 0) *last_piece = atomicAdd(a.counters + c0, 1) == c1 - c0;
-            named_barrier(1, 128);
+            named_barrier(1, kCompute);
+            int *counter = a.counters + c0 * a.heads + blockIdx.x % a.heads;
+            if (tid == 0) *last_piece = atomicAdd(counter, 1) == c1 - c0;
+            named_barrier(1, kCompute);
             if (*last_piece) {
                 __threadfence();
                 merge_pieces<D, R>(a, t, walk.s.cu0, walk.h, c0, c1, seg0 == c0 * found.run,
-                                   reinterpret_cast<float *>(p_s));
-                if (tid == 0) a.counters[c0] = 0;  // as the next call expects it
+                                   reinterpret_cast<float *>(p_s), tops_s);
+                if (tid == 0) *counter = 0;  // as the next call expects it
             }
         } else {
-            named_barrier(1, 128);  // tops and the Q buffer are free
+            named_barrier(1, kCompute);  // tops and the Q buffer are free
         }
     }
-    named_barrier(1, 128);
-    if (warp == 0) tmem_dealloc(tmem_s, T::TMEM);
+    tc_fence_before();
+    named_barrier(2, kCompute + 32);
 }
 
 template <int D, bool I8, int R>
@@ -860,7 +939,7 @@ cudaError_t launch(const PagedAttn &a, const CUtensorMap &tk, const CUtensorMap 
         split_attn_kernel<D, I8, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const int ctas = T::CTAS * num_sms < kSplitMaxCtas ? T::CTAS * num_sms : kSplitMaxCtas;
-    split_attn_kernel<D, I8, R><<<ctas, kThreads, smem, st>>>(tk, tv, a);
+    split_attn_kernel<D, I8, R><<<ctas / a.heads * a.heads, kThreads, smem, st>>>(tk, tv, a);
     return cudaGetLastError();
 }
 
@@ -868,8 +947,7 @@ template <int D, bool I8>
 cudaError_t launch_rows(const PagedAttn &a, int rows, const CUtensorMap &tk, const CUtensorMap &tv,
                         int num_sms, cudaStream_t st) {
     if (rows <= 8) return launch<D, I8, 8>(a, tk, tv, num_sms, st);
-    if (rows <= 16) return launch<D, I8, 16>(a, tk, tv, num_sms, st);
-    return launch<D, I8, 32>(a, tk, tv, num_sms, st);
+    return launch<D, I8, 16>(a, tk, tv, num_sms, st);
 }
 
 }  // namespace
