@@ -52,6 +52,7 @@ struct PagedAttn {
     float *lse = nullptr;    // fp32 [total][Hq]
     int Hq = 0, G = 0;
     int heads = 1;           // kv heads that share a run of key tiles (divides Hkv)
+    int row_lo = 0, row_hi = 0x7FFFFFFF;  // rows (tokens * G) of the sequences that a launch takes
     int window = 0, sinks = 0;       // window 0: every key up to the query's position
     const int32_t *ids = nullptr;    // sparse branch: [Bt][K] selected blocks (one row each)
     int K = 0, T = 0;                // sparse branch: selection width, common length
@@ -73,5 +74,10 @@ inline int split_box_rows(int block) { return block < kSplitKeys ? block : kSpli
 // knows; it chooses the tile height.
 cudaError_t launch_split_attn(const PagedAttn &a, int rows, const CUtensorMap &tk,
                               const CUtensorMap &tv, int num_sms, cudaStream_t st);
+
+constexpr int kChunkRows = 256;     // query rows per CTA of the chunk kernel
+constexpr int kChunkMaxCtas = 256;  // its CTAs, at most (workspace bound)
+cudaError_t launch_chunk_attn(const PagedAttn &a, const CUtensorMap &tk, const CUtensorMap &tv,
+                              int num_sms, cudaStream_t st);
 
 }  // namespace msa

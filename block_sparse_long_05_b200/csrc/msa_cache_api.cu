@@ -25,7 +25,11 @@ struct CacheWs {
 };
 
 CacheWs cache_layout(int d) {
-    const size_t rows = static_cast<size_t>(2) * kSplitMaxCtas * kSplitMaxRows;
+    // pieces of the split kernel, or of the chunk kernel: the calls that launch
+    // both run them one after the other
+    const size_t split = static_cast<size_t>(2) * kSplitMaxCtas * kSplitMaxRows;
+    const size_t chunk = static_cast<size_t>(2) * kChunkMaxCtas * kChunkRows;
+    const size_t rows = split > chunk ? split : chunk;
     CacheWs w;
     w.part_o = kWsHeader;
     w.part_lse = align_up(w.part_o + rows * d * 4, 256);
@@ -179,8 +183,21 @@ msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int nu
     if (!store_map(&tk, k_pages, num_pages, a.step.block, a.c.Hkv, a.c.d, box, i8) ||
         !store_map(&tv, v_pages, num_pages, a.step.block, a.c.Hkv, a.c.d, box, i8))
         return MSA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int rows = max_q < kSplitMaxRows ? max_q * a.G : kSplitMaxRows + 1;
-    const cudaError_t e = launch_split_attn(a, rows, tk, tv, sms, static_cast<cudaStream_t>(stream));
+    // the chunk kernel for the sequences with many rows, then (if there may be
+    // such) the split kernel for those with few; a hint that is too low costs
+    // time, not rows
+    cudaError_t e = cudaSuccess;
+    const bool chunk = rows > kSplitMaxRows && !a.ids;
+    if (chunk) {
+        a.row_lo = a.step.Bt > 1 ? kSplitMaxRows + 1 : 0;
+        e = launch_chunk_attn(a, tk, tv, sms, st);
+        a.row_lo = 0;
+        a.row_hi = kSplitMaxRows;
+    }
+    if (e == cudaSuccess && (!chunk || a.step.Bt > 1))
+        e = launch_split_attn(a, rows, tk, tv, sms, st);
     return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
 

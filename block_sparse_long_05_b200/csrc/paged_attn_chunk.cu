@@ -1,0 +1,721 @@
+// paged_attn_chunk.cu -- attention of a chunk of new tokens over a paged cache
+// (more than 16 query rows per sequence and kv head; formulas as in
+// paged_attn_split.cu).
+//
+// The matrix products bound it: 4 d flops per (row, key).  A CTA takes 256 rows
+// (i * G + g, token i, head g) of one kv head as two tiles of 128 and walks the
+// keys 128 at a time:
+//     S = Q K^T (tensor memory), P = 2^(S c - m) in bf16 over S, O += P V
+// with the two row tiles half a step apart, so that one tile's products run
+// while the other tile is in its softmax.  Both products read K and V from
+// shared memory as TMA left them; P never leaves tensor memory.  A softmax
+// thread has a whole row of S in registers: no shuffles.  The running
+// reference m is raised, and O rescaled, only when a score passes it by 2^8.
+//
+// int8 pages: four warps turn the codes into bf16 tiles (exact) ahead of the
+// products; the scales sk multiply the scores and sv the weights in fp32.
+//
+// P is rounded to bf16 (a relative error of at most 2^-8 per weight, averaged
+// over the keys; the sum l takes the unrounded values): the output's own
+// rounding is as large, and a second term would double the second product.
+//
+// The work is cut into equal runs of key tiles, one CTA per SM (paged_walk.cuh).
+// Segments in several runs leave fp32 pieces that a second kernel merges, 16
+// rows per CTA.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "cache.h"
+#include "msa_common.cuh"
+#include "paged_walk.cuh"
+#include "ptx_sm100.cuh"
+
+namespace msa {
+
+namespace {
+
+using namespace walk;
+
+constexpr int kRows = kChunkRows;
+constexpr int kMinRun = 4;     // tiles per run, at least
+constexpr int kMetaSlots = 8;  // tiles whose positions and scales are kept: more than
+                               // the rings of K and V tiles hold at a time
+constexpr float kLn2f = 0.6931471805599453f;
+
+template <int D, bool I8>
+struct Chunk {
+    static constexpr int REGS = D / 64;            // 128-byte wide regions of a bf16 tile
+    static constexpr int TILE = REGS * 128 * 128;  // bf16 tile: 128 rows
+    static constexpr int RAW = 128 * D;            // tile of codes
+    static constexpr int STAGES = I8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);  // bf16 tiles of K or V
+    static constexpr int RAWS = I8 ? (D == 128 ? 3 : 4) : 0;                     // tiles of codes
+    // warps 0-7: softmax; 8-11: int8 conversion; then a producer and a product warp
+    static constexpr int CONV = I8 ? 4 : 0;
+    static constexpr int THREADS = I8 ? 512 : 320;
+};
+
+struct alignas(16) TileMeta {
+    int pos;    // first key
+    int valid;  // bit i: keys 32 i .. 32 i + 31 are there
+    int pad[2];
+};
+
+template <int D, bool I8>
+constexpr size_t chunk_smem_bytes() {
+    using C = Chunk<D, I8>;
+    return 1024 + static_cast<size_t>(2 + C::STAGES) * C::TILE + C::RAWS * (C::RAW + 1024) +
+           kMetaSlots * (sizeof(TileMeta) + 8 + (I8 ? 1024 : 0)) +
+           (2 * C::STAGES + 2 * C::RAWS + 9) * 8 + 18 * 8 + 64;
+}
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            smem_addr(dst)),
+        "l"(src), "r"(bytes), "r"(smem_addr(bar))
+        : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Two signed bytes (the low bytes of the 16-bit halves of x) as bf16, exactly:
+// 128 + (low 7 bits), minus 128, or minus 256 where the sign bit is set.
+// 0x4300 is 128 in bf16, whose last mantissa bit counts 1; the byte's sign bit
+// falls on the lowest exponent bit, and 0x4380 is 256.
+__device__ __forceinline__ uint32_t s8x2_bf16(uint32_t x) {
+    const uint32_t hi = (x & 0x007F007Fu) | 0x43004300u, lo = (x & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&hi),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&lo));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+template <int D, bool I8>
+__global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const __grid_constant__ PagedAttn a) {
+    using C = Chunk<D, I8>;
+    constexpr int EB = I8 ? 1 : 2;
+    constexpr int RS = C::RAWS > 0 ? C::RAWS : 1;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *q_s = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));  // [row tile]
+    unsigned char *ring = q_s + 2 * C::TILE;             // [stage]
+    unsigned char *raw = ring + C::STAGES * C::TILE;     // [raw stage]
+    float *raw_sc = reinterpret_cast<float *>(raw + C::RAWS * C::RAW);   // [raw stage][K, V][128]
+    float *scales = raw_sc + C::RAWS * 256;                              // [slot][K, V][128]
+    TileMeta *meta = reinterpret_cast<TileMeta *>(scales + (I8 ? kMetaSlots * 256 : 0));
+    uint64_t *meta_full = reinterpret_cast<uint64_t *>(meta + kMetaSlots);
+    uint64_t *full = meta_full + kMetaSlots, *empty = full + C::STAGES;
+    uint64_t *raw_full = empty + C::STAGES, *raw_empty = raw_full + C::RAWS;
+    uint64_t *bar_s = raw_empty + C::RAWS;  // [row tile] scores complete
+    uint64_t *bar_o = bar_s + 2;            // [row tile] outputs complete
+    uint64_t *p_ready = bar_s + 4;          // [row tile] weights written
+    uint64_t *q_ready = bar_s + 6;          // [row tile] Q of a segment written
+    uint64_t *edge = bar_s + 8;             // a V tile that gets zeros
+    long long *scan = reinterpret_cast<long long *>(bar_s + 9);  // [18]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(scan + 18);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kProducer = 8 + C::CONV, kProducts = kProducer + 1;
+    if (tid == 0) {
+        for (int i = 0; i < kMetaSlots; ++i) mbar_init(meta_full + i, I8 ? 128 : 1);
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(full + i, I8 ? 128 : 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < C::RAWS; ++i) {
+            mbar_init(raw_full + i, 1);
+            mbar_init(raw_empty + i, 128);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_s + i, 1);
+            mbar_init(bar_o + i, 1);
+            mbar_init(p_ready + i, 128);
+            mbar_init(q_ready + i, 128);
+        }
+        mbar_init(edge, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    const Found found = find_run(a, kRows, kMinRun, scan);
+    if (found.start >= found.work) return;
+    if (warp == kProducts) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;  // S / P of the row tiles, then O of the row tiles: 128 columns each
+    Walk walk(found);
+    const int block = a.step.block;
+    // int8: 512 threads of 128 registers; 8 warps at 184 and 8 at 72 use them up.
+    // (Each branch begins with its warpgroup's request.)
+    if (warp >= 8) {
+    if (I8 && warp < kProducer) {
+        fewer_registers<72>();
+        // -------------------------------------------------------- int8 -> bf16
+        // Thread: one row of the tile; rows of 16-byte pieces, swizzled on both
+        // sides so that eight neighbouring rows fall on different banks.
+        const int r = tid & 127;
+        uint32_t e = 0, slot = 0;
+        bool ok = true;
+        auto convert = [&](bool is_v) {
+            const uint32_t rs = e % RS, st = e % C::STAGES;
+            ok = mbar_wait(raw_full + rs, (e / RS) & 1, abort_flag, a.status);
+            if (ok && e >= static_cast<uint32_t>(C::STAGES))
+                ok = mbar_wait(empty + st, ((e / C::STAGES) & 1) ^ 1, abort_flag, a.status);
+            if (!ok) return;
+            const unsigned char *src = raw + rs * C::RAW;
+            unsigned char *dst = ring + st * C::TILE;
+            if (!is_v) {
+                float *sc = scales + slot % kMetaSlots * 256;
+                sc[r] = raw_sc[rs * 256 + r];
+                sc[128 + r] = raw_sc[rs * 256 + 128 + r];
+                mbar_arrive(meta_full + slot % kMetaSlots);
+                ++slot;
+            }
+#pragma unroll
+            for (int p = 0; p < D / 16; ++p) {
+                const uint32_t at = D == 128 ? sw128_offset(r, p) : r * 64u + ((p ^ ((r >> 1) & 3u)) << 4);
+                const uint4 u = *reinterpret_cast<const uint4 *>(src + at);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[2 * i] = s8x2_bf16(__byte_perm(w[i], 0, 0x1100));
+                    o[2 * i + 1] = s8x2_bf16(__byte_perm(w[i], 0, 0x3322));
+                }
+                unsigned char *to = dst + p / 4 * 16384;
+                *reinterpret_cast<uint4 *>(to + sw128_offset(r, p % 4 * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(to + sw128_offset(r, p % 4 * 2 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(full + st);
+            mbar_arrive(raw_empty + rs);
+            ++e;
+        };
+        while (ok && walk.next(a, kRows)) {
+            const RowTile t = row_tile(a, walk.s, walk.rt, kRows);
+            const int n = min(walk.x1, t.count) - walk.x0;
+            for (int x = 0; x < n && ok; ++x) {
+                convert(false);
+                if (x > 0 && ok) convert(true);
+            }
+            if (n > 0 && ok) convert(true);
+        }
+        return;
+    }
+    if (I8) fewer_registers<72>();
+    if (warp == kProducer) {
+        // -------------------------------------------------------- producer
+        // Order of the tiles: K 0, then K x + 1 and V x in turn.
+        uint32_t e = 0, edges = 0;  // tiles issued; V tiles with zeros
+        uint32_t slot = 0;          // key tiles announced
+        const int box = min(block, kKeys);
+        bool ok = true;
+        // One tile of K or V: keys at pos.. (valid quarters), store rows z.  Some
+        // row of the segment sees the keys below hi that are sinks or from lo on.
+        auto load = [&](bool is_v, int pos, int valid, const int (&z)[4], int h, int lo, int hi, uint32_t sl) {
+            const uint32_t st = e % (I8 ? RS : C::STAGES), ph = e / (I8 ? RS : C::STAGES);
+            uint64_t *fb = I8 ? raw_full + st : full + st;
+            unsigned char *dst = I8 ? raw + st * C::RAW : ring + st * C::TILE;
+            // rows of V that no row may use are zeroed (bf16: they may hold anything,
+            // and 0 times it need not be 0)
+            const bool zeros = !I8 && is_v && (valid != 15 || pos + kKeys > hi || (pos < lo && pos + kKeys > a.sinks));
+            if (lane == 0) {
+                if (e >= static_cast<uint32_t>(I8 ? RS : C::STAGES))
+                    ok = mbar_wait((I8 ? raw_empty : empty) + st, (ph & 1) ^ 1, abort_flag, a.status);
+                if (ok) {
+                    if (!is_v) {
+                        meta[sl % kMetaSlots].pos = pos;
+                        meta[sl % kMetaSlots].valid = valid;
+                        if (!I8) mbar_arrive(meta_full + sl % kMetaSlots);
+                    }
+                    uint64_t *tb = zeros ? edge : fb;
+                    int boxes = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) boxes += i * 32 % box == 0 && (valid >> i & 1);
+                    if (boxes == 0)
+                        mbar_arrive(tb);
+                    else
+                        mbar_arrive_expect_tx(tb, boxes * box * (D * EB + (I8 && !is_v ? 8 : 0)));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (i * 32 % box != 0 || !(valid >> i & 1)) continue;
+                        if (I8) {
+                            tma_load_3d(dst + i * 32 * D, is_v ? &tm_v : &tm_k, tb, 0, h, z[i]);
+                            if (!is_v) {
+                                const int page = z[i] / block;
+                                const long long so = (static_cast<long long>(page) * a.c.Hkv + h) * block + (z[i] - page * block);
+                                bulk_load(raw_sc + st * 256 + i * 32, a.c.k_scales + so, box * 4, tb);
+                                bulk_load(raw_sc + st * 256 + 128 + i * 32, a.c.v_scales + so, box * 4, tb);
+                            }
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < C::REGS; ++r)
+                                tma_load_3d(dst + r * 16384 + i * 4096, is_v ? &tm_v : &tm_k, tb, r * 64, h, z[i]);
+                        }
+                    }
+                    if (zeros) ok = mbar_wait(edge, edges & 1, abort_flag, a.status);
+                }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (ok && zeros) {
+                ++edges;
+                mbar_try_wait(edge, (edges - 1) & 1);  // (complete: orders this lane's writes behind the copy's)
+                for (int r = lane; r < kKeys; r += 32) {
+                    const int p = pos + r;
+                    if ((valid >> (r / 32) & 1) && p < hi && (p >= lo || p < a.sinks)) continue;
+#pragma unroll
+                    for (int c = 0; c < 8 * C::REGS; ++c)
+                        *reinterpret_cast<uint4 *>(dst + c / 8 * 16384 + r * 128 + ((c + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(fb);
+            }
+            if (ok) ++e;
+        };
+        while (ok && walk.next(a, kRows)) {
+            const RowTile t = row_tile(a, walk.s, walk.rt, kRows);
+            const int x1 = min(walk.x1, t.count);
+            const int hi = min(t.tmax + 1, walk.s.cap);
+            const int lo = a.window ? t.tmin - a.window + 1 : 0;
+            int vp = 0, vv = 0, vz[4] = {0, 0, 0, 0};  // the V tile that follows the next K tile
+            for (int xb = walk.x0; xb < x1 && ok; xb += 32) {
+                int pos = 0, valid = 0, z[4] = {0, 0, 0, 0};
+                const int x = xb + lane;
+                if (x < x1) {
+                    pos = (x < t.na ? x : x + t.skip) * kKeys;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (i > 0 && i * 32 % box != 0) {
+                            valid |= (valid >> (i - 1) & 1) << i;
+                            continue;
+                        }
+                        const int p = pos + i * 32;
+                        if (p > t.tmax || p >= walk.s.cap) continue;
+                        const int j = p / block;
+                        const int page = a.step.pm.table[static_cast<long long>(walk.b) * a.step.pm.stride + j];
+                        if (page < 0 || page >= a.step.pm.count) {
+                            atomicOr(a.status, kDevBadIds);
+                            continue;
+                        }
+                        valid |= 1 << i;
+                        z[i] = page * block + (p - j * block);
+                    }
+                }
+                const int m = min(32, x1 - xb);
+                for (int y = 0; y < m && ok; ++y) {
+                    const int p = __shfl_sync(0xFFFFFFFFu, pos, y), v = __shfl_sync(0xFFFFFFFFu, valid, y);
+                    int zz[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) zz[i] = __shfl_sync(0xFFFFFFFFu, z[i], y);
+                    load(false, p, v, zz, walk.h, lo, hi, slot);
+                    ++slot;
+                    if (xb + y > walk.x0 && ok) load(true, vp, vv, vz, walk.h, lo, hi, 0);
+                    vp = p;
+                    vv = v;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vz[i] = zz[i];
+                }
+            }
+            if (ok && x1 > walk.x0) load(true, vp, vv, vz, walk.h, lo, hi, 0);
+        }
+        // after an abort: the copies have landed before the CTA ends
+        if (!ok && lane == 0) {
+            const uint32_t n = I8 ? RS : C::STAGES;
+            for (uint32_t i = e > n ? e - n : 0; i < e; ++i) {
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait((I8 ? raw_full : full) + i % n, (i / n) & 1))
+                    if (global_timer_ns() - t0 > kWaitLimitNs / 4) break;
+            }
+        }
+        return;
+    }
+
+    if (warp == kProducts) {
+        // -------------------------------------------------------- products
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false), idesc_o = idesc_bf16_f32(128, D, true);
+            const uint64_t q0 = sdesc_sw128(smem_addr(q_s), 16, 1024), k0 = sdesc_sw128(smem_addr(ring), 16, 1024);
+            const uint64_t v0 = sdesc_sw128(smem_addr(ring), 16384, 1024);
+            uint32_t e = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // ring tiles taken; Q and weights awaited
+            bool ok = true;
+            auto scores = [&](int t, uint32_t st) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t o = (k / 4) * 16384 + (k % 4) * 32;
+                    umma_bf16(tmem + t * 128, q0 + ((t * C::TILE + o) >> 4), k0 + ((st * C::TILE + o) >> 4), idesc_s, k > 0);
+                }
+                umma_commit(bar_s + t);
+            };
+            while (ok && walk.next(a, kRows)) {
+                const RowTile rt = row_tile(a, walk.s, walk.rt, kRows);
+                const int n = min(walk.x1, rt.count) - walk.x0;
+                const int tiles = rt.rows - rt.r0 > 128 ? 2 : 1;
+                for (int t = 0; t < tiles && ok; ++t) ok = mbar_wait(q_ready + t, nq[t]++ & 1, abort_flag, a.status);
+                if (!ok || n <= 0) continue;
+                uint32_t st = e % C::STAGES;
+                if (!(ok = mbar_wait(full + st, (e / C::STAGES) & 1, abort_flag, a.status))) break;
+                tc_fence_after();
+                for (int t = 0; t < tiles; ++t) scores(t, st);
+                umma_commit(empty + st);
+                ++e;
+                for (int x = 0; x < n && ok; ++x) {
+                    const bool more = x + 1 < n;
+                    const uint32_t ek = e, ev = more ? e + 1 : e;
+                    const uint32_t sk = ek % C::STAGES, sv = ev % C::STAGES;
+                    if (!(ok = mbar_wait(full + sv, (ev / C::STAGES) & 1, abort_flag, a.status))) break;
+                    for (int t = 0; t < tiles; ++t) {
+                        if (!(ok = mbar_wait(p_ready + t, np[t]++ & 1, abort_flag, a.status))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            umma_bf16_tmem_a(tmem + 256 + t * 128, tmem + t * 128 + k * 8,
+                                             v0 + ((sv * C::TILE + k * 16 * 128) >> 4), idesc_o, x > 0 || k > 0);
+                        umma_commit(bar_o + t);
+                        if (more) {
+                            if (t == 0 && !(ok = mbar_wait(full + sk, (ek / C::STAGES) & 1, abort_flag, a.status))) break;
+                            tc_fence_after();
+                            scores(t, sk);
+                        }
+                    }
+                    if (!ok) break;
+                    umma_commit(empty + sv);
+                    if (more) umma_commit(empty + sk);
+                    e = ev + 1;
+                }
+            }
+        }
+        __syncwarp();
+        named_barrier(2, 256 + 32);  // the softmax warps have read their last outputs
+        tmem_dealloc(tmem, 512);
+        return;
+    }
+
+    return;
+    }
+
+    if (I8) more_registers<184>();
+    // ------------------------------------------------------------ softmax
+    const int t = warp >> 2, row = tid & 127;  // row tile, row
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tmem_s = tmem + t * 128 + lanes, tmem_o = tmem + 256 + t * 128 + lanes;
+    const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2);
+    uint32_t slot = 0, n_s = 0;  // key tiles; products awaited
+    bool ok = true;
+    while (walk.next(a, kRows)) {
+        const RowTile rt = row_tile(a, walk.s, walk.rt, kRows);
+        const int x1 = min(walk.x1, rt.count);
+        const bool whole = walk.x0 == 0 && walk.x1 == walk.s.nk;
+        const bool idle = t == 1 && rt.rows - rt.r0 <= 128;  // no rows in this tile
+        const int first = rt.r0 + t * 128;                   // first row of the tile
+        // ---- Q rows of this tile into shared memory
+        if (!idle) {
+            constexpr int PPR = D / 8, STEP = 128 / PPR;
+            const int c = row % PPR;
+#pragma unroll 4
+            for (int r = row / PPR; r < 128; r += STEP) {
+                const int g = first + r, tok = g / a.G;
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (g < rt.rows)
+                    u = *reinterpret_cast<const uint4 *>(
+                        static_cast<const __nv_bfloat16 *>(a.q) + (walk.s.cu0 + tok) * a.q_stride +
+                        (static_cast<long long>(walk.h) * a.G + (g - tok * a.G)) * D + c * 8);
+                *reinterpret_cast<uint4 *>(q_s + t * C::TILE + (c / 8) * 16384 + sw128_offset(r, c % 8)) = u;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(q_ready + t);
+        }
+        const int mine = first + row, tok = mine / a.G;
+        const bool live = mine < rt.rows;
+        const int tpos = live ? min(walk.s.off + tok, walk.s.cap - 1) : -1;  // last key that the row sees
+        const int wpos = a.window && live ? walk.s.off + tok - a.window : -1;  // a key at or before it is out,
+                                                                               // unless a sink
+        // the tile's rows, for the choice of the masked path
+        const int tmin = walk.s.off + first / a.G;
+        const int tmax = walk.s.off + (min(first + 128, rt.rows) - 1) / a.G;
+
+        float m = -INFINITY, l = 0.f;
+        for (int x = walk.x0; x < x1; ++x, ++slot) {
+            if (idle || !ok) continue;
+            ok = mbar_wait(meta_full + slot % kMetaSlots, (slot / kMetaSlots) & 1, abort_flag, a.status) &&
+                 mbar_wait(bar_s + t, n_s & 1, abort_flag, a.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) continue;
+            tc_fence_after();
+            const int pos = meta[slot % kMetaSlots].pos, valid = meta[slot % kMetaSlots].valid;
+            const float *sk = scales + slot % kMetaSlots * 256, *sv = sk + 128;
+            const bool masked = valid != 15 || pos + kKeys - 1 > min(tmin, walk.s.cap - 1) ||
+                                (a.window && pos <= tmax - a.window && pos + kKeys > a.sinks);
+            const int lim = tpos - pos, low = wpos - pos, snk = a.window ? a.sinks - pos : 0;
+            uint64_t la = f2_pack(0.f, 0.f), lb = la;
+            uint32_t v[2][32];
+            tmem_ld32(tmem_s, v[0]);
+            // 32 keys at a time: scores, maximum, weights over the columns already read
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t(&y)[32] = v[c & 1];
+                tmem_wait_ld();
+                if (c < 3) tmem_ld32(tmem_s + (c + 1) * 32, v[c + 1 & 1]);
+                if (I8) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 k4 = *reinterpret_cast<const float4 *>(sk + c * 32 + i);
+                        float f0, f1, f2, f3;
+                        f2_unpack(f2_mul(f2_pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), f2_pack(k4.x, k4.y)), f0, f1);
+                        f2_unpack(f2_mul(f2_pack(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3])), f2_pack(k4.z, k4.w)), f2, f3);
+                        y[i] = __float_as_uint(f0);
+                        y[i + 1] = __float_as_uint(f1);
+                        y[i + 2] = __float_as_uint(f2);
+                        y[i + 3] = __float_as_uint(f3);
+                    }
+                }
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int k = c * 32 + i;
+                        if (k > lim || (k <= low && k >= snk) || !(valid >> c & 1)) y[i] = __float_as_uint(-INFINITY);
+                    }
+                }
+                float g4[4] = {__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]), __uint_as_float(y[3])};
+#pragma unroll
+                for (int i = 4; i < 28; i += 8) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) g4[k] = fmax3(g4[k], __uint_as_float(y[i + k]), __uint_as_float(y[i + 4 + k]));
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) g4[k] = fmaxf(g4[k], __uint_as_float(y[28 + k]));
+                const float g = fmaxf(fmax3(g4[0], g4[1], g4[2]), g4[3]) * a.scale_log2;
+                if (__any_sync(0xFFFFFFFFu, g > m + 8.f)) {
+                    // raise m: what was computed with the old one is rescaled -- O of the
+                    // tiles before (complete by now or soon), this tile's weights, l
+                    const float mn = fmaxf(m, g);
+                    const float f = m == -INFINITY ? 1.f : ex2_approx(m - mn);  // (nothing, or NaN, so far)
+                    m = mn;
+                    l *= f;
+                    la = f2_mul(la, f2_pack(f, f));
+                    lb = f2_mul(lb, f2_pack(f, f));
+                    if (c < 3) tmem_wait_ld();
+                    if (c > 0) tmem_wait_st();
+#pragma unroll 1
+                    for (int k = 0; k < c; ++k) {
+                        uint32_t w[16];
+                        tmem_ld16(tmem_s + k * 16, w);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = bf2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
+                        tmem_st16(tmem_s + k * 16, w);
+                    }
+                    if (x > walk.x0) {
+                        ok = ok && mbar_wait(bar_o + t, (n_s - 1) & 1, abort_flag, a.status);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int k = 0; k < D && ok; k += 16) {
+                            uint32_t w[16];
+                            tmem_ld16(tmem_o + k, w);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+                            tmem_st16(tmem_o + k, w);
+                        }
+                    }
+                }
+                const float mr = m == -INFINITY ? 0.f : m;
+                const uint64_t nm = f2_pack(-mr, -mr);
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float x0, x1_;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), c2, nm), x0, x1_);
+                    uint64_t p = f2_pack(ex2_approx(x0), ex2_approx(x1_));  // (masked columns: 0)
+                    if (i & 1)
+                        lb = f2_add(lb, p);
+                    else
+                        la = f2_add(la, p);
+                    if (I8) {
+                        const float2 s2 = *reinterpret_cast<const float2 *>(sv + c * 32 + 2 * i);
+                        p = f2_mul(p, f2_pack(s2.x, s2.y));
+                    }
+                    float p0, p1;
+                    f2_unpack(p, p0, p1);
+                    w[i] = bf2(p0, p1);
+                    if (I8 && masked) {  // a masked key's scale may hold anything
+                        if (y[2 * i] == 0xFF800000u) w[i] &= 0xFFFF0000u;
+                        if (y[2 * i + 1] == 0xFF800000u) w[i] &= 0x0000FFFFu;
+                    }
+                }
+                tmem_st16(tmem_s + c * 16, w);
+            }
+            float l0, l1, l2, l3;
+            f2_unpack(la, l0, l1);
+            f2_unpack(lb, l2, l3);
+            l += (l0 + l1) + (l2 + l3);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(p_ready + t);
+            ++n_s;
+        }
+
+        // ---- outputs: final, or a piece
+        const bool any = x1 > walk.x0 && !idle;
+        if (any && ok) ok = mbar_wait(bar_o + t, (n_s - 1) & 1, abort_flag, a.status);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (idle) continue;
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + __log2f(l);
+        const bool lead = walk.pos - (walk.x1 - walk.x0) == found.start;  // the run's first piece
+        const long long prow = (2ll * blockIdx.x + (lead ? 0 : 1)) * kRows + t * 128 + row;
+        const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (mine - tok * a.G);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            __syncwarp();
+            if (any && ok) {
+                tmem_ld32(tmem_o + c, o);
+                tmem_wait_ld();
+            }
+            if (!live) continue;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(any ? __uint_as_float(o[i]) * inv : 0.f);
+            if (whole) {
+                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    out[i] = make_uint4(bf2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
+                                        bf2(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
+                                        bf2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
+                                        bf2(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
+            } else {
+                uint4 *out = reinterpret_cast<uint4 *>(a.part_o + prow * D + c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+        }
+        if (live) {
+            if (whole)
+                a.lse[orow] = lse2 * kLn2f;
+            else
+                a.part_lse[prow] = lse2;
+        }
+        tc_fence_before();
+    }
+    named_barrier(2, 256 + 32);
+}
+
+// ===========================================================================
+// Merge of the segments that lie in several runs: CTAs (c, *) take the segment
+// that begins in run c and goes on into run c + 1, if there is one, 16 rows
+// each, a warp per row:  lse = log2 sum 2^lse_p,  out = sum 2^(lse_p - lse) o_p.
+// ===========================================================================
+constexpr int kMergeThreads = 512;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ PagedAttn a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces come from the previous kernel
+    __shared__ long long scan[18];
+    constexpr int COLS = D / 32;
+    const Found f = find_run(a, kRows, kMinRun, scan);
+    const long long next = f.start + f.run;
+    if (f.start >= f.work || next >= f.work) return;
+    // the segment of the run's last tile
+    Walk walk(f);
+    long long seg1 = 0, seg0 = 0;
+    while (walk.next(a, kRows)) {
+        seg0 = walk.pos - walk.x1;
+        seg1 = seg0 + walk.s.nk;
+    }
+    if (seg0 < f.start || seg1 <= next) return;  // begun earlier, or ends here
+    const int c0 = static_cast<int>(seg0 / f.run), pieces = static_cast<int>((seg1 - 1) / f.run) - c0 + 1;
+    const bool first = seg0 == f.start;
+    auto slot = [&](int p) { return 2ll * ((c0 + p) * a.heads + blockIdx.x % a.heads) + (p == 0 && !first ? 1 : 0); };
+    const int lane = threadIdx.x & 31, r = blockIdx.y * 16 + (threadIdx.x >> 5);
+    const int mine = walk.rt * kRows + r;
+    if (mine >= walk.s.n * a.G) return;
+    float acc[COLS], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < COLS; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < pieces; ++p) {
+        const long long at = slot(p) * kRows + r;
+        const float lp = a.part_lse[at];
+        float y[COLS];
+#pragma unroll
+        for (int e = 0; e < COLS; e += 2)
+            *reinterpret_cast<float2 *>(y + e) = *reinterpret_cast<const float2 *>(a.part_o + at * D + lane * COLS + e);
+        if (lp == -INFINITY) continue;  // no key of the row in this piece
+        const float g = fmaxf(top, lp), z = g == -INFINITY ? 0.f : g;
+        const float fo = top == -INFINITY ? (sum == 0.f ? 0.f : 1.f) : ex2_approx(top - z), w = ex2_approx(lp - z);
+        top = g;
+        sum = sum * fo + w;
+#pragma unroll
+        for (int e = 0; e < COLS; ++e) acc[e] = acc[e] * fo + w * y[e];
+    }
+    const int tok = mine / a.G;
+    const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (mine - tok * a.G);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t o[COLS / 2];
+#pragma unroll
+    for (int e = 0; e < COLS / 2; ++e) o[e] = bf2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + lane * COLS);
+#pragma unroll
+    for (int e = 0; e < COLS / 2; ++e) out[e] = o[e];
+    if (lane == 0) a.lse[orow] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) + __log2f(sum)) * kLn2f;
+}
+
+template <int D, bool I8>
+cudaError_t launch(const PagedAttn &a, const CUtensorMap &tk, const CUtensorMap &tv, int num_sms,
+                   cudaStream_t st) {
+    constexpr size_t smem = chunk_smem_bytes<D, I8>();
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    cudaError_t e = cudaFuncSetAttribute(chunk_attn_kernel<D, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int ctas = (num_sms < kChunkMaxCtas ? num_sms : kChunkMaxCtas) / a.heads * a.heads;
+    chunk_attn_kernel<D, I8><<<ctas, Chunk<D, I8>::THREADS, smem, st>>>(tk, tv, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, kRows / 16);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_attn(const PagedAttn &a, const CUtensorMap &tk, const CUtensorMap &tv,
+                              int num_sms, cudaStream_t st) {
+    if (a.c.d == 128)
+        return a.c.k_scales ? launch<128, true>(a, tk, tv, num_sms, st) : launch<128, false>(a, tk, tv, num_sms, st);
+    return a.c.k_scales ? launch<64, true>(a, tk, tv, num_sms, st) : launch<64, false>(a, tk, tv, num_sms, st);
+}
+
+}  // namespace msa
