@@ -20,8 +20,7 @@
 // rounding is as large, and a second term would double the second product.
 //
 // The work is cut into equal runs of key tiles, one CTA per SM (paged_walk.cuh).
-// Segments in several runs leave fp32 pieces that a second kernel merges, 16
-// rows per CTA.
+// Segments in several runs leave fp32 pieces that a second kernel merges.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -39,7 +38,8 @@ namespace {
 using namespace walk;
 
 constexpr int kRows = kChunkRows;
-constexpr int kMinRun = 4;     // tiles per run, at least
+constexpr int kOver = 4;       // a segment's start and end cost about as much as four tiles
+constexpr int kMinRun = 5;     // units per run, at least
 constexpr int kMetaSlots = 8;  // tiles whose positions and scales are kept: more than
                                // the rings of K and V tiles hold at a time
 constexpr float kLn2f = 0.6931471805599453f;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    const Found found = find_run(a, kRows, kMinRun, scan);
+    const Found found = find_run(a, kRows, kOver, kMinRun, scan);
     if (found.start >= found.work) return;
     if (warp == kProducts) {
         tmem_alloc(tmem_slot, 512);
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;  // S / P of the row tiles, then O of the row tiles: 128 columns each
-    Walk walk(found);
+    Walk walk(found, kOver);
     const int block = a.step.block;
     // int8: 512 threads of 128 registers; 8 warps at 184 and 8 at 72 use them up.
     // (Each branch begins with its warpgroup's request.)
@@ -426,23 +426,26 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     while (walk.next(a, kRows)) {
         const RowTile rt = row_tile(a, walk.s, walk.rt, kRows);
         const int x1 = min(walk.x1, rt.count);
-        const bool whole = walk.x0 == 0 && walk.x1 == walk.s.nk;
+        const bool whole = walk.whole;
         const bool idle = t == 1 && rt.rows - rt.r0 <= 128;  // no rows in this tile
         const int first = rt.r0 + t * 128;                   // first row of the tile
         // ---- Q rows of this tile into shared memory
         if (!idle) {
             constexpr int PPR = D / 8, STEP = 128 / PPR;
             const int c = row % PPR;
-#pragma unroll 4
-            for (int r = row / PPR; r < 128; r += STEP) {
-                const int g = first + r, tok = g / a.G;
-                uint4 u = make_uint4(0, 0, 0, 0);
+            uint4 u[PPR];  // (all in flight)
+#pragma unroll
+            for (int i = 0; i < PPR; ++i) {
+                const int g = first + row / PPR + i * STEP, tok = g / a.G;
+                u[i] = make_uint4(0, 0, 0, 0);
                 if (g < rt.rows)
-                    u = *reinterpret_cast<const uint4 *>(
+                    u[i] = *reinterpret_cast<const uint4 *>(
                         static_cast<const __nv_bfloat16 *>(a.q) + (walk.s.cu0 + tok) * a.q_stride +
                         (static_cast<long long>(walk.h) * a.G + (g - tok * a.G)) * D + c * 8);
-                *reinterpret_cast<uint4 *>(q_s + t * C::TILE + (c / 8) * 16384 + sw128_offset(r, c % 8)) = u;
             }
+#pragma unroll
+            for (int i = 0; i < PPR; ++i)
+                *reinterpret_cast<uint4 *>(q_s + t * C::TILE + (c / 8) * 16384 + sw128_offset(row / PPR + i * STEP, c % 8)) = u[i];
             fence_proxy_async_smem();
             mbar_arrive(q_ready + t);
         }
@@ -586,8 +589,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + __log2f(l);
-        const bool lead = walk.pos - (walk.x1 - walk.x0) == found.start;  // the run's first piece
-        const long long prow = (2ll * blockIdx.x + (lead ? 0 : 1)) * kRows + t * 128 + row;
+        const long long prow = walk.slot(found) * kRows + t * 128 + row;
         const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (mine - tok * a.G);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -627,62 +629,74 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
 
 // ===========================================================================
 // Merge of the segments that lie in several runs: CTAs (c, *) take the segment
-// that begins in run c and goes on into run c + 1, if there is one, 16 rows
-// each, a warp per row:  lse = log2 sum 2^lse_p,  out = sum 2^(lse_p - lse) o_p.
+// that begins in run c and goes on into run c + 1, if there is one, 64 rows
+// each, 8 per warp:  lse = log2 sum 2^lse_p,  out = sum 2^(lse_p - lse) o_p.
 // ===========================================================================
-constexpr int kMergeThreads = 512;
+constexpr int kMergeThreads = 256, kMergeRows = 64;  // 8 rows per warp
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ PagedAttn a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces come from the previous kernel
     __shared__ long long scan[18];
-    constexpr int COLS = D / 32;
-    const Found f = find_run(a, kRows, kMinRun, scan);
-    const long long next = f.start + f.run;
+    constexpr int COLS = D / 32, RW = kMergeRows * 32 / kMergeThreads;
+    Found f = find_run(a, kRows, kOver, kMinRun, scan, true);
+    const long long next = f.start + f.run, start = f.start;
     if (f.start >= f.work || next >= f.work) return;
-    // the segment of the run's last tile
-    Walk walk(f);
-    long long seg1 = 0, seg0 = 0;
-    while (walk.next(a, kRows)) {
-        seg0 = walk.pos - walk.x1;
-        seg1 = seg0 + walk.s.nk;
-    }
-    if (seg0 < f.start || seg1 <= next) return;  // begun earlier, or ends here
-    const int c0 = static_cast<int>(seg0 / f.run), pieces = static_cast<int>((seg1 - 1) / f.run) - c0 + 1;
-    const bool first = seg0 == f.start;
-    auto slot = [&](int p) { return 2ll * ((c0 + p) * a.heads + blockIdx.x % a.heads) + (p == 0 && !first ? 1 : 0); };
-    const int lane = threadIdx.x & 31, r = blockIdx.y * 16 + (threadIdx.x >> 5);
-    const int mine = walk.rt * kRows + r;
-    if (mine >= walk.s.n * a.G) return;
-    float acc[COLS], top = -INFINITY, sum = 0.f;
+    // the segment of the run's last unit
+    f.start = next - 1;
+    Walk walk(f, kOver);
+    walk.end = next;
+    if (!walk.next(a, kRows) || walk.tile0 < start || walk.end0 <= next) return;  // begun earlier, or ends here
+    f.start = start;
+    const int c0 = walk.first_run(f), pieces = walk.last_run(f) - c0 + 1;
+    const int lane = threadIdx.x & 31, r0 = blockIdx.y * kMergeRows + (threadIdx.x >> 5) * RW;
+    const int rows = min(walk.s.n * a.G - walk.rt * kRows, kRows);
+    if (r0 >= rows) return;
+    float acc[RW][COLS], top[RW], sum[RW];
 #pragma unroll
-    for (int e = 0; e < COLS; ++e) acc[e] = 0.f;
-#pragma unroll 4
+    for (int r = 0; r < RW; ++r) {
+        top[r] = -INFINITY;
+        sum[r] = 0.f;
+#pragma unroll
+        for (int e = 0; e < COLS; ++e) acc[r][e] = 0.f;
+    }
+#pragma unroll 2
     for (int p = 0; p < pieces; ++p) {
-        const long long at = slot(p) * kRows + r;
-        const float lp = a.part_lse[at];
-        float y[COLS];
+        const long long row0 = piece_slot(a, c0, p) * kRows + r0;
+        const float lp = lane < RW && r0 + lane < rows ? a.part_lse[row0 + lane] : -INFINITY;
+        float y[RW][COLS];
+#pragma unroll
+        for (int r = 0; r < RW; ++r)
+#pragma unroll
+            for (int e = 0; e < COLS; e += 2) {
+                float2 u = make_float2(0.f, 0.f);
+                if (r0 + r < rows) u = *reinterpret_cast<const float2 *>(a.part_o + (row0 + r) * D + lane * 2 + e * 32);
+                y[r][e] = u.x;
+                y[r][e + 1] = u.y;
+            }
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            const float l = __shfl_sync(0xFFFFFFFFu, lp, r);
+            const float g = fmaxf(top[r], l), z = g == -INFINITY ? 0.f : g;
+            const float fo = ex2_approx(top[r] - z), w = ex2_approx(l - z);
+            top[r] = g;
+            sum[r] = sum[r] * fo + w;
+#pragma unroll
+            for (int e = 0; e < COLS; ++e) acc[r][e] = acc[r][e] * fo + (l == -INFINITY ? 0.f : w * y[r][e]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+        if (r0 + r >= rows) break;
+        const int mine = walk.rt * kRows + r0 + r, tok = mine / a.G;
+        const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (mine - tok * a.G);
+        const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
 #pragma unroll
         for (int e = 0; e < COLS; e += 2)
-            *reinterpret_cast<float2 *>(y + e) = *reinterpret_cast<const float2 *>(a.part_o + at * D + lane * COLS + e);
-        if (lp == -INFINITY) continue;  // no key of the row in this piece
-        const float g = fmaxf(top, lp), z = g == -INFINITY ? 0.f : g;
-        const float fo = top == -INFINITY ? (sum == 0.f ? 0.f : 1.f) : ex2_approx(top - z), w = ex2_approx(lp - z);
-        top = g;
-        sum = sum * fo + w;
-#pragma unroll
-        for (int e = 0; e < COLS; ++e) acc[e] = acc[e] * fo + w * y[e];
+            *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + lane * 2 + e * 32) =
+                bf2(acc[r][e] * inv, acc[r][e + 1] * inv);
+        if (lane == 0) a.lse[orow] = sum[r] == 0.f ? -INFINITY : ((top[r] == -INFINITY ? 0.f : top[r]) + __log2f(sum[r])) * kLn2f;
     }
-    const int tok = mine / a.G;
-    const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (mine - tok * a.G);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint32_t o[COLS / 2];
-#pragma unroll
-    for (int e = 0; e < COLS / 2; ++e) o[e] = bf2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + lane * COLS);
-#pragma unroll
-    for (int e = 0; e < COLS / 2; ++e) out[e] = o[e];
-    if (lane == 0) a.lse[orow] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) + __log2f(sum)) * kLn2f;
 }
 
 template <int D, bool I8>
@@ -698,7 +712,7 @@ cudaError_t launch(const PagedAttn &a, const CUtensorMap &tk, const CUtensorMap 
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, kRows / 16);
+    cfg.gridDim = dim3(ctas, kRows / kMergeRows);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];

@@ -61,7 +61,8 @@ using namespace walk;
 constexpr int kCompute = 256;                // warps 0-3 and 4-7, alternate tiles: one key (then
                                              // one value column) per thread
 constexpr int kThreads = kCompute + 64;      // warp 8: producer; warp 9: products
-constexpr int kMinRun = 2;  // tiles per run: below it the merge costs more than the run saves
+constexpr int kOver = 2;    // a segment's start and end cost about as much as two tiles
+constexpr int kMinRun = 3;  // units per run, at least
 constexpr float kLn2f = 0.6931471805599453f;
 
 // ------------------------------------------------------------ tile geometry
@@ -93,9 +94,6 @@ struct alignas(16) StageMeta {
 };
 
 constexpr int kScaleBytes = 2 * kKeys * 4;  // K and V scales of a stage
-constexpr int kMergeFloats = 1024;          // weights of a chunk of pieces, 8 rows at a time
-                                            // (in the buffer of P)
-
 template <int D, bool I8, int R>
 constexpr size_t split_smem_bytes() {
     using T = Tile<D, I8, R>;
@@ -156,86 +154,92 @@ __device__ __forceinline__ uint64_t col_desc(uint32_t addr) {
 constexpr uint32_t kIdescAMn = 1u << 15;  // A runs along M in memory
 
 // ===========================================================================
-// Merge of the pieces of a segment whose first run is c0 and last run c1:
+// Merge of the pieces of a segment that begins in run c0:
 //   lse = log2 sum 2^lse_p,  out = sum 2^(lse_p - lse) o_p
-// by the compute threads: a value column and half of the rows each.
-// wt: kMergeFloats weights, tops: [R] maxima.
+// by the compute warps: every eighth piece each, 4 rows at a time, a lane
+// D / 32 columns of all 4, then over the warps in shared memory (pool: 8 KB,
+// tops: 64 floats).
 // ===========================================================================
 template <int D, int R>
 __device__ __noinline__ void merge_pieces(const PagedAttn &a, const RowTile &t, int cu0, int h, int c0,
-                                          int c1, bool first, float *wt, float *tops) {
-    constexpr int CH = kMergeFloats / 8;  // pieces per chunk
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int pieces = c1 - c0 + 1, live = min(t.rows - t.r0, R);
-    // the first run's piece is its last one, unless the run begins with it
-    auto slot = [&](int p) { return 2ll * ((c0 + p) * a.heads + blockIdx.x % a.heads) + (p == 0 && !first ? 1 : 0); };
-    // a warp finds the maximum of a row over all pieces
-    for (int r = warp; r < live; r += kCompute / 32) {
-        float g = -INFINITY;
-        for (int p = lane; p < pieces; p += 32) g = fmaxf(g, __ldcg(a.part_lse + slot(p) * R + r));
-        g = warp_max(g);
-        if (lane == 0) tops[r] = g;
-    }
-    named_barrier(1, kCompute);
-    constexpr int RH = 4;  // rows of a thread at a time
-    const int col = (tid & 127) < D ? tid & 127 : 0;
+                                          int pieces, float *pool, float *tops) {
+    constexpr int RG = 4, COLS = D / 32, WARPS = kCompute / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int live = min(t.rows - t.r0, R);
+    float2 *ml = reinterpret_cast<float2 *>(tops);  // [warp][row] (maximum, sum)
 #pragma unroll 1
-    for (int rg = 0; rg < live; rg += 2 * RH) {
-        const int r0 = rg + (tid >> 7) * RH;  // (the two halves of the threads)
-        float acc[RH], sum[RH];
+    for (int rg = 0; rg < live; rg += RG) {
+        float acc[RG][COLS], top[RG], sum[RG];
 #pragma unroll
-        for (int r = 0; r < RH; ++r) acc[r] = sum[r] = 0.f;
+        for (int r = 0; r < RG; ++r) {
+            top[r] = -INFINITY;
+            sum[r] = 0.f;
+#pragma unroll
+            for (int e = 0; e < COLS; ++e) acc[r][e] = 0.f;
+        }
 #pragma unroll 1
-        for (int p0 = 0; p0 < pieces; p0 += CH) {
-            const int m = min(CH, pieces - p0);
-            for (int e = tid; e < m * 2 * RH; e += kCompute) {
-                const int r = rg + e % (2 * RH);
-                float w = 0.f;  // 0: the piece has no key of the row
-                if (r < live) {
-                    const float l = __ldcg(a.part_lse + slot(p0 + e / (2 * RH)) * R + r), g = tops[r];
-                    // (a weight that underflows stays above 0, for the sake of a NaN)
-                    if (l != -INFINITY) {
-                        w = ex2_approx(l - (g == -INFINITY ? 0.f : g));
-                        if (w == 0.f) w = 1.2e-38f;
-                    }
+        for (int p = warp; p < pieces; p += WARPS) {
+            const long long row0 = piece_slot(a, c0, p) * R + rg;
+            const float lp = lane < RG && rg + lane < live ? __ldcg(a.part_lse + row0 + lane) : -INFINITY;
+            float y[RG][COLS];
+#pragma unroll
+            for (int r = 0; r < RG; ++r)
+#pragma unroll
+                for (int e = 0; e < COLS; e += 2) {
+                    float2 u = make_float2(0.f, 0.f);
+                    if (rg + r < live) u = __ldcg(reinterpret_cast<const float2 *>(a.part_o + (row0 + r) * D + lane * 2 + e * 32));
+                    y[r][e] = u.x;
+                    y[r][e + 1] = u.y;
                 }
-                wt[e] = w;
+#pragma unroll
+            for (int r = 0; r < RG; ++r) {
+                const float l = __shfl_sync(0xFFFFFFFFu, lp, r);
+                // (no key of this row in the piece: weight 0, whatever y holds)
+                const float g = fmaxf(top[r], l), z = g == -INFINITY ? 0.f : g;
+                const float f = ex2_approx(top[r] - z), w = ex2_approx(l - z);
+                top[r] = g;
+                sum[r] = sum[r] * f + w;
+#pragma unroll
+                for (int e = 0; e < COLS; ++e) acc[r][e] = acc[r][e] * f + (l == -INFINITY ? 0.f : w * y[r][e]);
             }
+        }
+        if (lane == 0) {
+#pragma unroll
+            for (int r = 0; r < RG; ++r) ml[warp * RG + r] = make_float2(top[r], sum[r]);
+        }
+        named_barrier(1, kCompute);
+        constexpr int ROWS = 2;  // rows at a time: [warp][ROWS][D] in the pool
+#pragma unroll
+        for (int q = 0; q < RG; q += ROWS) {
+            if (rg + q >= live) break;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                for (int e = 0; e < COLS; e += 2)
+                    *reinterpret_cast<float2 *>(pool + (warp * ROWS + r) * D + lane * 2 + e * 32) = make_float2(acc[q + r][e], acc[q + r][e + 1]);
             named_barrier(1, kCompute);
-#pragma unroll 1
-            for (int p = 0; p < m; p += 4) {
-                float y[4][RH];
+            const int r = threadIdx.x / D, col = threadIdx.x % D;
+            if (r < ROWS && rg + q + r < live) {
+                float g = -INFINITY, s = 0.f, x = 0.f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int w = 0; w < WARPS; ++w) g = fmaxf(g, ml[w * RG + q + r].x);
+                const float z = g == -INFINITY ? 0.f : g;
 #pragma unroll
-                    for (int r = 0; r < RH; ++r)
-                        y[k][r] = p + k < m && r0 + r < live ? __ldcg(a.part_o + (slot(p0 + p + k) * R + r0 + r) * D + col) : 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (p + k >= m) break;
-                    const float4 w4 = *reinterpret_cast<const float4 *>(wt + (p + k) * 2 * RH + (tid >> 7) * RH);
-                    const float w[RH] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                    for (int r = 0; r < RH; ++r) {
-                        sum[r] += w[r];
-                        acc[r] += w[r] == 0.f ? 0.f : w[r] * y[k][r];
-                    }
+                for (int w = 0; w < WARPS; ++w) {
+                    const float2 y = ml[w * RG + q + r];
+                    const float f = y.x == -INFINITY ? 1.f : ex2_approx(y.x - z);  // (-inf: nothing, or NaN)
+                    s += y.y * f;
+                    x += pool[(w * ROWS + r) * D + col] * f;
                 }
+                const int row = t.r0 + rg + q + r, tok = row / a.G;
+                const long long orow = (static_cast<long long>(cu0) + tok) * a.Hq + static_cast<long long>(h) * a.G + (row - tok * a.G);
+                const float inv = s == 0.f ? 0.f : 1.f / s;
+                static_cast<__nv_bfloat16 *>(a.out)[orow * D + col] = __float2bfloat16_rn(x * inv);
+                if (col == 0) a.lse[orow] = s == 0.f ? -INFINITY : (z + __log2f(s)) * kLn2f;
             }
             named_barrier(1, kCompute);
         }
-#pragma unroll
-        for (int r = 0; r < RH; ++r) {
-            if (r0 + r >= live || (tid & 127) >= D) continue;
-            const int row = t.r0 + r0 + r, tok = row / a.G;
-            const long long orow = (static_cast<long long>(cu0) + tok) * a.Hq + static_cast<long long>(h) * a.G + (row - tok * a.G);
-            const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r], g = tops[r0 + r];
-            static_cast<__nv_bfloat16 *>(a.out)[orow * D + (tid & 127)] = __float2bfloat16_rn(acc[r] * inv);
-            if ((tid & 127) == 0)
-                a.lse[orow] = sum[r] == 0.f ? -INFINITY : ((g == -INFINITY ? 0.f : g) + __log2f(sum[r])) * kLn2f;
-        }
     }
-    named_barrier(1, kCompute);
 }
 
 // ===========================================================================
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
     unsigned char *q_s = ring + T::STAGES * T::STAGE;
     unsigned char *p_s = q_s + round_up(T::QBYTES, 1024);
     float *scales = reinterpret_cast<float *>(p_s + 2 * round_up(T::PBYTES, 1024));  // [stage][K, V][128]
-    static_assert(T::PBYTES >= kMergeFloats * 4, "merge weights");
+    static_assert(2 * round_up(T::PBYTES, 1024) >= 8192 && 8 * (R + 4) >= 64, "merge buffers");
     constexpr int TW = R + 4;  // maxima of a warp: its rows' scores, then its V scales
     float *tops_s = scales + (I8 ? T::STAGES * 2 * kKeys : 0);     // [warp][TW]
     float *qscale = tops_s + 8 * TW;                               // [R] factor of a row's scores
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
     if (tid < kCompute) {  // rows of the operand buffer that no digit or head ever fills
         for (int e = tid; e < T::QBYTES / 16; e += kCompute) reinterpret_cast<uint4 *>(q_s)[e] = make_uint4(0, 0, 0, 0);
     }
-    const Found found = find_run(a, R, kMinRun, scan);  // (its barriers order the writes above)
+    const Found found = find_run(a, R, kOver, kMinRun, scan);  // (its barriers order the writes above)
     if (found.start >= found.work) return;
     if (warp == 9) {
         tmem_alloc(tmem_slot, T::TMEM);
@@ -303,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;  // per warpgroup: NS columns of scores, NO of outputs
-    Walk walk(found);
+    Walk walk(found, kOver);
     const int block = a.step.block;
 
     if (warp == 8) {
@@ -477,7 +481,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
     while (walk.next(a, R)) {
         const RowTile t = row_tile(a, walk.s, walk.rt, R);
         const int x1 = min(walk.x1, t.count);
-        const bool whole = walk.x0 == 0 && walk.x1 == walk.s.nk;
         // ---- Q rows into shared memory, 16 threads per row (8 with d = 64)
         constexpr int TPR = D / 8;
 #pragma unroll
@@ -706,8 +709,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
 #pragma unroll
         for (int r = 0; r < R / 2; ++r) pool[(r + wg * (R / 2)) * 128 + key] = wg ? o[r] : o[R / 2 + r];
         named_barrier(1, kCompute);
-        const bool lead = walk.pos - (walk.x1 - walk.x0) == found.start;  // the run's first piece
-        const long long prow = (2ll * blockIdx.x + (lead ? 0 : 1)) * R;
+        const long long prow = walk.slot(found) * R;
 #pragma unroll
         for (int e = 0; e < R / 2; ++e) {
             const int r = wg * (R / 2) + e, row = t.r0 + r;
@@ -723,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
             if (I8 && poison[r]) inv = __uint_as_float(0x7FC00000u);
             const float y = (mine * f0 + other * f1) * inv;
             const float lse2 = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) + __log2f(sum);
-            if (whole) {
+            if (walk.whole) {
                 const int tok = row / a.G;
                 const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq +
                                        static_cast<long long>(walk.h) * a.G + (row - tok * a.G);
@@ -734,19 +736,17 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                 if (key == 0) a.part_lse[prow + r] = lse2;
             }
         }
-        if (!whole) {
-            // pieces of this segment: one per run that holds a part of it
-            const long long seg0 = walk.pos - walk.x1, seg1 = seg0 + walk.s.nk;
-            const int c0 = static_cast<int>(seg0 / found.run), c1 = static_cast<int>((seg1 - 1) / found.run);
+        if (!walk.whole) {
+            // the last of the segment's pieces to be finished merges them
+            const int c0 = walk.first_run(found), c1 = walk.last_run(found);
+            int *counter = a.counters + c0 * a.heads + blockIdx.x % a.heads;
             __threadfence();
             named_barrier(1, kCompute);
-            int *counter = a.counters + c0 * a.heads + blockIdx.x % a.heads;
             if (tid == 0) *last_piece = atomicAdd(counter, 1) == c1 - c0;
             named_barrier(1, kCompute);
             if (*last_piece) {
                 __threadfence();
-                merge_pieces<D, R>(a, t, walk.s.cu0, walk.h, c0, c1, seg0 == c0 * found.run,
-                                   reinterpret_cast<float *>(p_s), tops_s);
+                merge_pieces<D, R>(a, t, walk.s.cu0, walk.h, c0, c1 - c0 + 1, reinterpret_cast<float *>(p_s), tops_s);
                 if (tid == 0) *counter = 0;  // as the next call expects it
             }
         } else {

@@ -56,8 +56,10 @@ __device__ __forceinline__ Seq seq_of(const PagedAttn &a, int b, int R) {
     return s;
 }
 
-__device__ __forceinline__ long long seq_work(const PagedAttn &a, const Seq &s) {
-    return static_cast<long long>(s.nt) * (a.c.Hkv / a.heads) * s.nk;
+// Work of a sequence in units: its key tiles, and `over` more per segment for
+// what a segment costs beside them (reading Q, writing the output).
+__device__ __forceinline__ long long seq_work(const PagedAttn &a, const Seq &s, int over) {
+    return static_cast<long long>(s.nt) * (a.c.Hkv / a.heads) * (s.nk + over);
 }
 
 // Row tile rt of a sequence: positions of its rows and its key tiles.  Tile
@@ -92,14 +94,14 @@ __device__ __forceinline__ RowTile row_tile(const PagedAttn &a, const Seq &s, in
 }
 
 // Where a run begins: sequence and offset in it.  CTAs blockIdx.x / heads share
-// a run of at least `least` tiles.  All threads of the CTA take
+// a run of at least `least` units.  All threads of the CTA take
 // part; blockDim is a multiple of 32 and at most 512.
 struct Found {
     int b;
     long long off;
-    long long work;   // tiles of the step
-    long long start;  // first tile of this CTA's run
-    long long run;    // tiles per run
+    long long work;   // units of the step
+    long long start;  // first unit of this CTA's run
+    long long run;    // units per run
 };
 
 __device__ __forceinline__ long long run_length(long long work, int ctas, int least) {
@@ -108,7 +110,8 @@ __device__ __forceinline__ long long run_length(long long work, int ctas, int le
 }
 
 // sm: [0..15] warp sums, [16] sequence, [17] offset
-__device__ __forceinline__ Found find_run(const PagedAttn &a, int R, int least, long long *sm) {
+// `end`: the place of the run's last unit instead of its first one.
+__device__ __forceinline__ Found find_run(const PagedAttn &a, int R, int over, int least, long long *sm, bool end = false) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const int Bt = a.step.Bt, chunks = (Bt + blockDim.x - 1) / blockDim.x;
     auto work_of = [&](int b) -> long long {
@@ -116,7 +119,7 @@ __device__ __forceinline__ Found find_run(const PagedAttn &a, int R, int least, 
         const Seq s = seq_of(a, b, R);
         // a context longer than its page-table row: the keys past it do not exist
         if (s.off + s.n > s.cap) atomicOr(a.status, kDevBadIds);
-        return seq_work(a, s);
+        return seq_work(a, s, over);
     };
     Found f;
     f.b = 0;
@@ -134,6 +137,7 @@ __device__ __forceinline__ Found find_run(const PagedAttn &a, int R, int least, 
     f.run = run_length(f.work, gridDim.x / a.heads, least);
     f.start = f.run * (blockIdx.x / a.heads);
     if (f.start >= f.work) return f;
+    const long long u = end ? min(f.start + f.run, f.work) - 1 : f.start;
     long long base = 0;
     for (int c = 0; c < chunks; ++c) {
         const long long x = chunks == 1 ? mine : work_of(c * blockDim.x + threadIdx.x);
@@ -152,12 +156,12 @@ __device__ __forceinline__ Found find_run(const PagedAttn &a, int R, int least, 
             all += sm[i];
         }
         const long long first = before + p - x;
-        if (f.start >= first && f.start < first + x) {
+        if (u >= first && u < first + x) {
             sm[16] = c * static_cast<int>(blockDim.x) + threadIdx.x;
-            sm[17] = f.start - first;
+            sm[17] = u - first;
         }
         base += all;
-        if (f.start < base) break;
+        if (u < base) break;
     }
     __syncthreads();
     f.b = static_cast<int>(sm[16]);
@@ -165,36 +169,70 @@ __device__ __forceinline__ Found find_run(const PagedAttn &a, int R, int least, 
     return f;
 }
 
-// A run's segments in order: sequence, row tile, kv head, key tiles [x0, x1).
+// A run's pieces of segments in order: sequence, row tile, kv head, key tiles
+// [x0, x1).  A segment's extra units come before its tiles; a run that ends
+// among them has no piece of it.
 struct Walk {
     Seq s;
     int b, rt, h, x0, x1;
+    bool whole;            // all tiles of the segment
+    long long tile0, end0;  // units of the segment's first tile, and behind its last one
     long long pos, end, off;
-    __device__ __forceinline__ explicit Walk(const Found &f)
-        : b(f.b), pos(f.start), end(min(f.start + f.run, f.work)), off(f.off) {}
+    int over;
+    __device__ __forceinline__ Walk(const Found &f, int over_)
+        : b(f.b), pos(f.start), end(min(f.start + f.run, f.work)), off(f.off), over(over_) {}
     __device__ __forceinline__ bool next(const PagedAttn &a, int R) {
-        if (pos >= end) return false;
-        s = seq_of(a, b, R);
-        while (off >= seq_work(a, s)) {  // (only after a step; bounded by Bt)
-            off = 0;
-            if (++b >= a.step.Bt) return false;
+        while (pos < end) {
             s = seq_of(a, b, R);
+            while (off >= seq_work(a, s, over)) {  // (only after a step; bounded by Bt)
+                off = 0;
+                if (++b >= a.step.Bt) return false;
+                s = seq_of(a, b, R);
+            }
+            const int chunks = a.c.Hkv / a.heads, units = s.nk + over;
+            int seg, u0;  // segment of the sequence, unit of the segment
+            if (off >> 31) {
+                const long long y = off / units;
+                seg = static_cast<int>(y);
+                u0 = static_cast<int>(off - y * units);
+            } else {
+                seg = static_cast<int>(off) / units;
+                u0 = static_cast<int>(off) - seg * units;
+            }
+            const int y = seg / chunks;
+            h = (seg - y * chunks) * a.heads + blockIdx.x % a.heads;
+            // last, first, last but one, ...: in a causal chunk late row tiles have more
+            // keys than early ones, and a run of several gets its share of both
+            rt = y & 1 ? y / 2 : s.nt - 1 - y / 2;
+            const long long left = end - pos;
+            const int u1 = left < units - u0 ? u0 + static_cast<int>(left) : units;
+            tile0 = pos - u0 + over;
+            end0 = pos - u0 + units;
+            pos += u1 - u0;
+            off += u1 - u0;
+            if (u1 <= over) continue;
+            x0 = max(u0 - over, 0);
+            x1 = u1 - over;
+            whole = x0 == 0 && x1 == s.nk;
+            return true;
         }
-        const long long seg = off / s.nk;
-        const int chunks = a.c.Hkv / a.heads;
-        x0 = static_cast<int>(off - seg * s.nk);
-        const int y = static_cast<int>(seg / chunks);
-        h = static_cast<int>(seg - static_cast<long long>(y) * chunks) * a.heads + blockIdx.x % a.heads;
-        // last, first, last but one, ...: in a causal chunk late row tiles have more
-        // keys than early ones, and a run of several gets its share of both
-        rt = y & 1 ? y / 2 : s.nt - 1 - y / 2;
-        const long long left = end - pos;
-        x1 = left < s.nk - x0 ? x0 + static_cast<int>(left) : s.nk;
-        pos += x1 - x0;
-        off += x1 - x0;
-        return true;
+        return false;
     }
+    // Where the piece goes that is not the whole segment (per row tile and
+    // head): a run has at most one that goes on from the run before (slot 0) and
+    // one that goes on into the next run (slot 1).
+    __device__ __forceinline__ long long slot(const Found &f) const {
+        return 2ll * blockIdx.x + (tile0 >= f.start ? 1 : 0);
+    }
+    // First and last run with a piece of the segment.
+    __device__ __forceinline__ int first_run(const Found &f) const { return static_cast<int>(tile0 / f.run); }
+    __device__ __forceinline__ int last_run(const Found &f) const { return static_cast<int>((end0 - 1) / f.run); }
 };
+
+// Slot of piece p of a segment that begins in run c0 (its heads' CTAs share it).
+__device__ __forceinline__ long long piece_slot(const PagedAttn &a, int c0, int p) {
+    return 2ll * ((c0 + p) * a.heads + blockIdx.x % a.heads) + (p == 0 ? 1 : 0);
+}
 
 }  // namespace walk
 
