@@ -51,9 +51,15 @@ struct Chunk {
     static constexpr int RAW = 128 * D;            // tile of codes
     static constexpr int STAGES = I8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);  // bf16 tiles of K or V
     static constexpr int RAWS = I8 ? (D == 128 ? 3 : 4) : 0;                     // tiles of codes
-    // warps 0-7: softmax; 8-11: int8 conversion; then a producer and a product warp
+    // warps 0-15: softmax; 16-19: int8 conversion; then a producer and a product
+    // warp, and two that fill up their warpgroup.  Registers per thread: at launch
+    // THREADS * LAUNCH of the SM's 65536, then split anew.
     static constexpr int CONV = I8 ? 4 : 0;
-    static constexpr int THREADS = I8 ? 512 : 320;
+    static constexpr int THREADS = I8 ? 768 : 640;
+    static constexpr int LAUNCH = I8 ? 80 : 96;
+    static constexpr int REST = I8 ? 48 : 64;
+    static constexpr int SOFTMAX = I8 ? 96 : 104;
+    static_assert(512 * SOFTMAX + (THREADS - 512) * REST <= THREADS * LAUNCH && THREADS * LAUNCH <= 65536, "registers");
 };
 
 struct alignas(16) TileMeta {
@@ -65,8 +71,8 @@ struct alignas(16) TileMeta {
 template <int D, bool I8>
 constexpr size_t chunk_smem_bytes() {
     using C = Chunk<D, I8>;
-    return 1024 + static_cast<size_t>(2 + C::STAGES) * C::TILE + C::RAWS * (C::RAW + 1024) +
-           kMetaSlots * (sizeof(TileMeta) + 8 + (I8 ? 1024 : 0)) +
+    return static_cast<size_t>(2 + C::STAGES) * C::TILE + C::RAWS * (C::RAW + 1024) +
+           kMetaSlots * (sizeof(TileMeta) + 8 + (I8 ? 1024 : 0)) + 2048 +
            (2 * C::STAGES + 2 * C::RAWS + 9) * 8 + 18 * 8 + 64;
 }
 
@@ -110,14 +116,13 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     using C = Chunk<D, I8>;
     constexpr int EB = I8 ? 1 : 2;
     constexpr int RS = C::RAWS > 0 ? C::RAWS : 1;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *q_s = reinterpret_cast<unsigned char *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));  // [row tile]
+    extern __shared__ __align__(1024) unsigned char q_s[];  // [row tile]
     unsigned char *ring = q_s + 2 * C::TILE;             // [stage]
     unsigned char *raw = ring + C::STAGES * C::TILE;     // [raw stage]
     float *raw_sc = reinterpret_cast<float *>(raw + C::RAWS * C::RAW);   // [raw stage][K, V][128]
     float *scales = raw_sc + C::RAWS * 256;                              // [slot][K, V][128]
-    TileMeta *meta = reinterpret_cast<TileMeta *>(scales + (I8 ? kMetaSlots * 256 : 0));
+    float *halves = scales + (I8 ? kMetaSlots * 256 : 0);  // [row tile][half][row]: maxima, then sums
+    TileMeta *meta = reinterpret_cast<TileMeta *>(halves + 512);
     uint64_t *meta_full = reinterpret_cast<uint64_t *>(meta + kMetaSlots);
     uint64_t *full = meta_full + kMetaSlots, *empty = full + C::STAGES;
     uint64_t *raw_full = empty + C::STAGES, *raw_empty = raw_full + C::RAWS;
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kProducer = 8 + C::CONV, kProducts = kProducer + 1;
+    constexpr int kProducer = 16 + C::CONV, kProducts = kProducer + 1;
     if (tid == 0) {
         for (int i = 0; i < kMetaSlots; ++i) mbar_init(meta_full + i, I8 ? 128 : 1);
         for (int i = 0; i < C::STAGES; ++i) {
@@ -145,8 +150,8 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_s + i, 1);
             mbar_init(bar_o + i, 1);
-            mbar_init(p_ready + i, 128);
-            mbar_init(q_ready + i, 128);
+            mbar_init(p_ready + i, 256);
+            mbar_init(q_ready + i, 256);
         }
         mbar_init(edge, 1);
         *abort_flag = 0;
@@ -166,11 +171,10 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     const uint32_t tmem = *tmem_slot;  // S / P of the row tiles, then O of the row tiles: 128 columns each
     Walk walk(found, kOver);
     const int block = a.step.block;
-    // int8: 512 threads of 128 registers; 8 warps at 184 and 8 at 72 use them up.
-    // (Each branch begins with its warpgroup's request.)
-    if (warp >= 8) {
+    // (each branch begins with its warpgroup's register request)
+    if (warp >= 16) {
     if (I8 && warp < kProducer) {
-        fewer_registers<72>();
+        fewer_registers<C::REST>();
         // -------------------------------------------------------- int8 -> bf16
         // Thread: one row of the tile; rows of 16-byte pieces, swizzled on both
         // sides so that eight neighbouring rows fall on different banks.
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
         }
         return;
     }
-    if (I8) fewer_registers<72>();
+    fewer_registers<C::REST>();
     if (warp == kProducer) {
         // -------------------------------------------------------- producer
         // Order of the tiles: K 0, then K x + 1 and V x in turn.
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                         tc_fence_after();
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k)
-                            umma_bf16_tmem_a(tmem + 256 + t * 128, tmem + t * 128 + k * 8,
+                            umma_bf16_tmem_a(tmem + 256 + t * 128, tmem + t * 128 + (k / 4) * 64 + (k % 4) * 8,
                                              v0 + ((sv * C::TILE + k * 16 * 128) >> 4), idesc_o, x > 0 || k > 0);
                         umma_commit(bar_o + t);
                         if (more) {
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
             }
         }
         __syncwarp();
-        named_barrier(2, 256 + 32);  // the softmax warps have read their last outputs
+        named_barrier(2, 512 + 32);  // the softmax warps have read their last outputs
         tmem_dealloc(tmem, 512);
         return;
     }
@@ -415,28 +419,31 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     return;
     }
 
-    if (I8) more_registers<184>();
+    more_registers<C::SOFTMAX>();
     // ------------------------------------------------------------ softmax
-    const int t = warp >> 2, row = tid & 127;  // row tile, row
+    // Two warpgroups per row tile, 64 of a tile's 128 keys each; a thread has a
+    // row.  Its weights go over the first half of its own score columns.
+    const int t = warp >> 3, half = warp >> 2 & 1, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tmem_s = tmem + t * 128 + lanes, tmem_o = tmem + 256 + t * 128 + lanes;
+    const uint32_t tmem_s = tmem + t * 128 + half * 64 + lanes, tmem_o = tmem + 256 + t * 128 + half * (D / 2) + lanes;
     const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2);
+    float *mine_x = halves + (t * 2 + half) * 128 + row;
+    const float *other_x = halves + (t * 2 + (half ^ 1)) * 128 + row;
     uint32_t slot = 0, n_s = 0;  // key tiles; products awaited
     bool ok = true;
     while (walk.next(a, kRows)) {
         const RowTile rt = row_tile(a, walk.s, walk.rt, kRows);
         const int x1 = min(walk.x1, rt.count);
-        const bool whole = walk.whole;
         const bool idle = t == 1 && rt.rows - rt.r0 <= 128;  // no rows in this tile
         const int first = rt.r0 + t * 128;                   // first row of the tile
         // ---- Q rows of this tile into shared memory
         if (!idle) {
-            constexpr int PPR = D / 8, STEP = 128 / PPR;
-            const int c = row % PPR;
-            uint4 u[PPR];  // (all in flight)
+            constexpr int PPR = D / 8, STEP = 256 / PPR;
+            const int c = row % PPR, r0 = (row + half * 128) / PPR;
+            uint4 u[PPR / 2];  // (all in flight)
 #pragma unroll
-            for (int i = 0; i < PPR; ++i) {
-                const int g = first + row / PPR + i * STEP, tok = g / a.G;
+            for (int i = 0; i < PPR / 2; ++i) {
+                const int g = first + r0 + i * STEP, tok = g / a.G;
                 u[i] = make_uint4(0, 0, 0, 0);
                 if (g < rt.rows)
                     u[i] = *reinterpret_cast<const uint4 *>(
@@ -444,8 +451,8 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                         (static_cast<long long>(walk.h) * a.G + (g - tok * a.G)) * D + c * 8);
             }
 #pragma unroll
-            for (int i = 0; i < PPR; ++i)
-                *reinterpret_cast<uint4 *>(q_s + t * C::TILE + (c / 8) * 16384 + sw128_offset(row / PPR + i * STEP, c % 8)) = u[i];
+            for (int i = 0; i < PPR / 2; ++i)
+                *reinterpret_cast<uint4 *>(q_s + t * C::TILE + (c / 8) * 16384 + sw128_offset(r0 + i * STEP, c % 8)) = u[i];
             fence_proxy_async_smem();
             mbar_arrive(q_ready + t);
         }
@@ -455,7 +462,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
         const int wpos = a.window && live ? walk.s.off + tok - a.window : -1;  // a key at or before it is out,
                                                                                // unless a sink
         // the tile's rows, for the choice of the masked path
-        const int tmin = walk.s.off + first / a.G;
+        const int tmin = min(walk.s.off + first / a.G, walk.s.cap - 1);
         const int tmax = walk.s.off + (min(first + 128, rt.rows) - 1) / a.G;
 
         float m = -INFINITY, l = 0.f;
@@ -463,23 +470,16 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
             if (idle || !ok) continue;
             ok = mbar_wait(meta_full + slot % kMetaSlots, (slot / kMetaSlots) & 1, abort_flag, a.status) &&
                  mbar_wait(bar_s + t, n_s & 1, abort_flag, a.status);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) continue;
+            __syncwarp();
             tc_fence_after();
             const int pos = meta[slot % kMetaSlots].pos, valid = meta[slot % kMetaSlots].valid;
-            const float *sk = scales + slot % kMetaSlots * 256, *sv = sk + 128;
-            const bool masked = valid != 15 || pos + kKeys - 1 > min(tmin, walk.s.cap - 1) ||
+            const float *sk = scales + slot % kMetaSlots * 256 + half * 64, *sv = sk + 128;
+            const bool masked = valid != 15 || pos + kKeys - 1 > tmin ||
                                 (a.window && pos <= tmax - a.window && pos + kKeys > a.sinks);
-            const int lim = tpos - pos, low = wpos - pos, snk = a.window ? a.sinks - pos : 0;
-            uint64_t la = f2_pack(0.f, 0.f), lb = la;
-            uint32_t v[2][32];
-            tmem_ld32(tmem_s, v[0]);
-            // 32 keys at a time: scores, maximum, weights over the columns already read
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t(&y)[32] = v[c & 1];
+            // 32 scores, times sk; keys that the row does not see are -inf
+            auto scores = [&](int c, uint32_t(&y)[32]) {
+                tmem_ld32(tmem_s + c * 32, y);
                 tmem_wait_ld();
-                if (c < 3) tmem_ld32(tmem_s + (c + 1) * 32, v[c + 1 & 1]);
                 if (I8) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
@@ -493,66 +493,84 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                         y[i + 3] = __float_as_uint(f3);
                     }
                 }
+            };
+            // keys of the 32 that the row sees, one bit each
+            auto visible = [&](int c) -> uint32_t {
+                auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
+                const int k0 = pos + half * 64 + c * 32;
+                uint32_t bits = below(tpos + 1 - k0);
+                if (a.window) bits &= ~below(wpos + 1 - k0) | below(a.sinks - k0);
+                return valid >> (half * 2 + c) & 1 ? bits : 0u;
+            };
+            // ---- the row's maximum
+            float g = -INFINITY;
+            // (not unrolled: copies of the body run slower, for want of instruction cache)
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+                uint32_t y[32];
+                scores(c, y);
                 if (masked) {
+                    const uint32_t bits = visible(c);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int k = c * 32 + i;
-                        if (k > lim || (k <= low && k >= snk) || !(valid >> c & 1)) y[i] = __float_as_uint(-INFINITY);
-                    }
+                    for (int i = 0; i < 32; ++i) y[i] = bits >> i & 1 ? y[i] : 0xFF800000u;
                 }
-                float g4[4] = {__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]), __uint_as_float(y[3])};
+                float g4[4] = {g, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 4; i < 28; i += 8) {
+                for (int i = 0; i < 32; i += 8)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) g4[k] = fmax3(g4[k], __uint_as_float(y[i + k]), __uint_as_float(y[i + 4 + k]));
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) g4[k] = fmaxf(g4[k], __uint_as_float(y[28 + k]));
-                const float g = fmaxf(fmax3(g4[0], g4[1], g4[2]), g4[3]) * a.scale_log2;
-                if (__any_sync(0xFFFFFFFFu, g > m + 8.f)) {
-                    // raise m: what was computed with the old one is rescaled -- O of the
-                    // tiles before (complete by now or soon), this tile's weights, l
-                    const float mn = fmaxf(m, g);
-                    const float f = m == -INFINITY ? 1.f : ex2_approx(m - mn);  // (nothing, or NaN, so far)
-                    m = mn;
-                    l *= f;
-                    la = f2_mul(la, f2_pack(f, f));
-                    lb = f2_mul(lb, f2_pack(f, f));
-                    if (c < 3) tmem_wait_ld();
-                    if (c > 0) tmem_wait_st();
+                g = fmaxf(fmax3(g4[0], g4[1], g4[2]), g4[3]);
+            }
+            g *= a.scale_log2;
+            // Weights and sums are floating point numbers, so the reference m may lag
+            // behind the maximum: it is raised (with O and l) when a score of some row of
+            // the tile passes it by 2^32, and at first.
+            if (named_barrier_or(3 + t, 256, g > m + 32.f || !ok)) {
+                *mine_x = g;
+                named_barrier(3 + t, 256);
+                const float mn = fmaxf(m, fmaxf(g, *other_x));
+                const float f = m == -INFINITY ? 1.f : ex2_approx(m - mn);  // (nothing, or NaN, so far)
+                m = mn;
+                l *= f;
+                if (x > walk.x0) {  // O of the tiles before, complete by now or soon
+                    ok = ok && mbar_wait(bar_o + t, (n_s - 1) & 1, abort_flag, a.status);
+                    __syncwarp();
+                    tc_fence_after();
 #pragma unroll 1
-                    for (int k = 0; k < c; ++k) {
+                    for (int k = 0; k < D / 2; k += 16) {
                         uint32_t w[16];
-                        tmem_ld16(tmem_s + k * 16, w);
+                        tmem_ld16(tmem_o + k, w);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            w[i] = bf2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
-                        tmem_st16(tmem_s + k * 16, w);
-                    }
-                    if (x > walk.x0) {
-                        ok = ok && mbar_wait(bar_o + t, (n_s - 1) & 1, abort_flag, a.status);
-                        ok = __all_sync(0xFFFFFFFFu, ok);
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int k = 0; k < D && ok; k += 16) {
-                            uint32_t w[16];
-                            tmem_ld16(tmem_o + k, w);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-                            tmem_st16(tmem_o + k, w);
-                        }
+                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+                        tmem_st16(tmem_o + k, w);
                     }
                 }
-                const float mr = m == -INFINITY ? 0.f : m;
-                const uint64_t nm = f2_pack(-mr, -mr);
-                uint32_t w[16];
+                // (*other_x is read before it is written again: a whole tile lies between)
+                if (named_barrier_or(3 + t, 256, !ok)) {
+                    ok = false;
+                    continue;
+                }
+            }
+            // ---- the weights, over score columns that have been read
+            const float mr = m == -INFINITY ? 0.f : m;
+            const uint64_t nm = f2_pack(-mr, -mr);
+            uint64_t la = f2_pack(0.f, 0.f), lb = la;
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+                uint32_t y[32], w[16];
+                scores(c, y);
+                uint32_t bits = 0xFFFFFFFFu;
+                if (masked) {
+                    bits = visible(c);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) y[i] = bits >> i & 1 ? y[i] : 0xFF800000u;
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    float x0, x1_;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), c2, nm), x0, x1_);
-                    uint64_t p = f2_pack(ex2_approx(x0), ex2_approx(x1_));  // (masked columns: 0)
+                    float e0, e1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), c2, nm), e0, e1);
+                    uint64_t p = f2_pack(ex2_approx(e0), ex2_approx(e1));  // (masked columns: 0)
                     if (i & 1)
                         lb = f2_add(lb, p);
                     else
@@ -564,10 +582,11 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                     float p0, p1;
                     f2_unpack(p, p0, p1);
                     w[i] = bf2(p0, p1);
-                    if (I8 && masked) {  // a masked key's scale may hold anything
-                        if (y[2 * i] == 0xFF800000u) w[i] &= 0xFFFF0000u;
-                        if (y[2 * i + 1] == 0xFF800000u) w[i] &= 0x0000FFFFu;
-                    }
+                }
+                if (I8 && masked) {  // a masked key's scale may hold anything
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[i] &= (bits >> (2 * i) & 1 ? 0x0000FFFFu : 0u) | (bits >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
                 }
                 tmem_st16(tmem_s + c * 16, w);
             }
@@ -580,30 +599,32 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
             mbar_arrive(p_ready + t);
             ++n_s;
         }
-
-        // ---- outputs: final, or a piece
-        const bool any = x1 > walk.x0 && !idle;
-        if (any && ok) ok = mbar_wait(bar_o + t, (n_s - 1) & 1, abort_flag, a.status);
-        ok = __all_sync(0xFFFFFFFFu, ok);
         if (idle) continue;
+
+        // ---- outputs: final, or a piece; half of the columns each
+        const bool any = x1 > walk.x0;
+        *mine_x = l;
+        named_barrier(3 + t, 256);
+        l += *other_x;
+        if (any) ok = ok && mbar_wait(bar_o + t, (n_s - 1) & 1, abort_flag, a.status);
+        __syncwarp();
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + __log2f(l);
         const long long prow = walk.slot(found) * kRows + t * 128 + row;
         const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (mine - tok * a.G);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D / 2; c += 32) {
             uint32_t o[32];
             __syncwarp();
-            if (any && ok) {
-                tmem_ld32(tmem_o + c, o);
-                tmem_wait_ld();
-            }
+            tmem_ld32(tmem_o + c, o);
+            tmem_wait_ld();
             if (!live) continue;
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(any ? __uint_as_float(o[i]) * inv : 0.f);
-            if (whole) {
-                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + c);
+            const int col = half * (D / 2) + c;
+            if (walk.whole) {
+                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + col);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     out[i] = make_uint4(bf2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
@@ -611,20 +632,21 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                                         bf2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
                                         bf2(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
             } else {
-                uint4 *out = reinterpret_cast<uint4 *>(a.part_o + prow * D + c);
+                uint4 *out = reinterpret_cast<uint4 *>(a.part_o + prow * D + col);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
         }
-        if (live) {
-            if (whole)
+        if (live && half == 0) {
+            if (walk.whole)
                 a.lse[orow] = lse2 * kLn2f;
             else
                 a.part_lse[prow] = lse2;
         }
         tc_fence_before();
+        ok = !named_barrier_or(3 + t, 256, !ok);  // (sums are read before the next segment's maxima)
     }
-    named_barrier(2, 256 + 32);
+    named_barrier(2, 512 + 32);
 }
 
 // ===========================================================================
