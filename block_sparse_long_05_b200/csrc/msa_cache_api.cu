@@ -184,7 +184,15 @@ msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int nu
         !store_map(&tv, v_pages, num_pages, a.step.block, a.c.Hkv, a.c.d, box, i8))
         return MSA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int rows = max_q < kSplitMaxRows ? max_q * a.G : kSplitMaxRows + 1;
+    // (a hint below the average is wrong)
+    const long long mean = (static_cast<long long>(a.step.total) + a.step.Bt - 1) / a.step.Bt;
+    const long long most = (max_q > mean ? max_q : mean) * a.G;
+    const int rows = most <= kSplitMaxRows ? static_cast<int>(most) : kSplitMaxRows + 1;
+    // work units are numbered with 31 bits: row tiles x head groups x key tiles
+    const long long all = static_cast<long long>(a.step.total) * a.G;
+    const long long tiles = a.ids || rows <= kSplitMaxRows ? all / 8 + a.step.Bt : all / 256 + 2 * a.step.Bt;
+    const long long keys = a.ids ? static_cast<long long>(a.K) * a.step.block : static_cast<long long>(a.step.pm.stride) * a.step.block;
+    if (tiles * (a.c.Hkv / a.heads) * (keys / kSplitKeys + 8) >= (1ll << 31)) return MSA_ERR_UNSUPPORTED;
     // the chunk kernel for the sequences with many rows, then (if there may be
     // such) the split kernel for those with few; a hint that is too low costs
     // time, not rows

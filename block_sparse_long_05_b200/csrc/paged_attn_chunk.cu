@@ -73,7 +73,7 @@ constexpr size_t chunk_smem_bytes() {
     using C = Chunk<D, I8>;
     return static_cast<size_t>(2 + C::STAGES) * C::TILE + C::RAWS * (C::RAW + 1024) +
            kMetaSlots * (sizeof(TileMeta) + 8 + (I8 ? 1024 : 0)) + 2048 +
-           (2 * C::STAGES + 2 * C::RAWS + 9) * 8 + 18 * 8 + 64;
+           (2 * C::STAGES + 2 * C::RAWS + 9) * 8 + 64;
 }
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -131,8 +131,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     uint64_t *p_ready = bar_s + 4;          // [row tile] weights written
     uint64_t *q_ready = bar_s + 6;          // [row tile] Q of a segment written
     uint64_t *edge = bar_s + 8;             // a V tile that gets zeros
-    long long *scan = reinterpret_cast<long long *>(bar_s + 9);  // [18]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(scan + 18);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_s + 9);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -159,7 +158,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    const Found found = find_run(a, kRows, kOver, kMinRun, scan);
+    const Found found = find_run(a, kRows, kOver, kMinRun);
     if (found.start >= found.work) return;
     if (warp == kProducts) {
         tmem_alloc(tmem_slot, 512);
@@ -169,7 +168,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;  // S / P of the row tiles, then O of the row tiles: 128 columns each
-    Walk walk(found, kOver);
+    Walk walk(a, found, kOver);
     const int block = a.step.block;
     // (each branch begins with its warpgroup's register request)
     if (warp >= 16) {
@@ -659,14 +658,14 @@ constexpr int kMergeThreads = 256, kMergeRows = 64;  // 8 rows per warp
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ PagedAttn a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces come from the previous kernel
-    __shared__ long long scan[18];
     constexpr int COLS = D / 32, RW = kMergeRows * 32 / kMergeThreads;
-    Found f = find_run(a, kRows, kOver, kMinRun, scan, true);
-    const long long next = f.start + f.run, start = f.start;
-    if (f.start >= f.work || next >= f.work) return;
+    Found f = find_run(a, kRows, kOver, kMinRun, true);
+    const int start = f.start;
+    if (f.start >= f.work || f.run >= f.work - f.start) return;
+    const int next = f.start + f.run;
     // the segment of the run's last unit
     f.start = next - 1;
-    Walk walk(f, kOver);
+    Walk walk(a, f, kOver);
     walk.end = next;
     if (!walk.next(a, kRows) || walk.tile0 < start || walk.end0 <= next) return;  // begun earlier, or ends here
     f.start = start;

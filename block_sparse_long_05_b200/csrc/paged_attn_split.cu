@@ -98,7 +98,7 @@ template <int D, bool I8, int R>
 constexpr size_t split_smem_bytes() {
     using T = Tile<D, I8, R>;
     return 1024 + static_cast<size_t>(T::STAGES) * T::STAGE + round_up(T::QBYTES, 1024) +
-           2 * round_up(T::PBYTES, 1024) + (I8 ? T::STAGES * kScaleBytes : 0) + 2 * (R + 4) * 16 + R * 36 + 16 + T::STAGES * (sizeof(StageMeta) + 16) + 216;
+           2 * round_up(T::PBYTES, 1024) + (I8 ? T::STAGES * kScaleBytes : 0) + 2 * (R + 4) * 16 + R * 36 + 16 + T::STAGES * (sizeof(StageMeta) + 16) + 72;
 }
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -272,8 +272,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
     uint64_t *bar_o = bar_s + 2;          // [warpgroup] outputs complete
     uint64_t *p_ready = bar_s + 4;        // [warpgroup] weights written, scores and last outputs read
     uint64_t *q_ready = bar_s + 6;        // Q of a segment written
-    long long *scan = reinterpret_cast<long long *>(bar_s + 7);  // [18]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(scan + 18);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_s + 7);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *last_piece = abort_flag + 1;
 
@@ -297,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
     if (tid < kCompute) {  // rows of the operand buffer that no digit or head ever fills
         for (int e = tid; e < T::QBYTES / 16; e += kCompute) reinterpret_cast<uint4 *>(q_s)[e] = make_uint4(0, 0, 0, 0);
     }
-    const Found found = find_run(a, R, kOver, kMinRun, scan);  // (its barriers order the writes above)
+    const Found found = find_run(a, R, kOver, kMinRun);
     if (found.start >= found.work) return;
     if (warp == 9) {
         tmem_alloc(tmem_slot, T::TMEM);
@@ -307,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;  // per warpgroup: NS columns of scores, NO of outputs
-    Walk walk(found, kOver);
+    Walk walk(a, found, kOver);
     const int block = a.step.block;
 
     if (warp == 8) {
@@ -690,13 +689,21 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
         // ---- end of the segment: the rows' sums over the key lanes, then both
         // warpgroups' results (merge buffer: the weights', which are all read)
         named_barrier(1, kCompute);  // (both have their last outputs)
+        // (halving the rows with each exchange: lane i ends with row i / (32 / R))
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float y = l[r];
+        for (int k = 16, n = R / 2; k; k >>= 1, n >>= 1) {
+            const bool up = lane & k;
+            if (n) {
 #pragma unroll
-            for (int k = 16; k; k >>= 1) y += __shfl_xor_sync(0xFFFFFFFFu, y, k);
-            if (lane == 0) tops[quarter * TW + r] = y;
+                for (int r = 0; r < n; ++r) {
+                    const float send = up ? l[r] : l[r + n], keep = up ? l[r + n] : l[r];
+                    l[r] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, k);
+                }
+            } else {
+                l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], k);
+            }
         }
+        if (lane % (32 / R) == 0) tops[quarter * TW + lane / (32 / R)] = l[0];
         named_barrier(3 + wg, 128);
         if (key < R) {
             sums[wg * R + key] = (tops[key] + tops[TW + key]) + (tops[2 * TW + key] + tops[3 * TW + key]);
@@ -740,9 +747,11 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
             // the last of the segment's pieces to be finished merges them
             const int c0 = walk.first_run(found), c1 = walk.last_run(found);
             int *counter = a.counters + c0 * a.heads + blockIdx.x % a.heads;
-            __threadfence();
             named_barrier(1, kCompute);
-            if (tid == 0) *last_piece = atomicAdd(counter, 1) == c1 - c0;
+            if (tid == 0) {
+                __threadfence();  // (the barrier has ordered the other threads' writes before it)
+                *last_piece = atomicAdd(counter, 1) == c1 - c0;
+            }
             named_barrier(1, kCompute);
             if (*last_piece) {
                 __threadfence();

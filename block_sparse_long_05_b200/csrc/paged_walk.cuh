@@ -15,6 +15,7 @@ namespace msa {
 namespace walk {
 
 constexpr int kKeys = kSplitKeys;  // keys per tile
+constexpr int kAlignUnits = 10;    // units that a run may grow by to end with a segment
 
 // Sequence b of a step, in rows and key tiles.
 struct Seq {
@@ -57,9 +58,10 @@ __device__ __forceinline__ Seq seq_of(const PagedAttn &a, int b, int R) {
 }
 
 // Work of a sequence in units: its key tiles, and `over` more per segment for
-// what a segment costs beside them (reading Q, writing the output).
-__device__ __forceinline__ long long seq_work(const PagedAttn &a, const Seq &s, int over) {
-    return static_cast<long long>(s.nt) * (a.c.Hkv / a.heads) * (s.nk + over);
+// what a segment costs beside them (reading Q, writing the output).  (The host
+// keeps the units of a step below 2^31.)
+__device__ __forceinline__ int seq_work(const PagedAttn &a, const Seq &s, int over) {
+    return s.nt * (a.c.Hkv / a.heads) * (s.nk + over);
 }
 
 // Row tile rt of a sequence: positions of its rows and its key tiles.  Tile
@@ -93,79 +95,87 @@ __device__ __forceinline__ RowTile row_tile(const PagedAttn &a, const Seq &s, in
     return t;
 }
 
-// Where a run begins: sequence and offset in it.  CTAs blockIdx.x / heads share
-// a run of at least `least` units.  All threads of the CTA take
-// part; blockDim is a multiple of 32 and at most 512.
+// Where a run begins: sequence (and what seq_of says of it) and offset in it.
+// CTAs blockIdx.x / heads share a run of at least `least` units.
 struct Found {
-    int b;
-    long long off;
-    long long work;   // units of the step
-    long long start;  // first unit of this CTA's run
-    long long run;    // units per run
+    Seq s;
+    int b, off;
+    int work;   // units of the step
+    int start;  // first unit of this CTA's run
+    int run;    // units per run
 };
 
-__device__ __forceinline__ long long run_length(long long work, int ctas, int least) {
-    const long long per = (work + ctas - 1) / ctas;
-    return per > least ? per : least;
-}
-
-// sm: [0..15] warp sums, [16] sequence, [17] offset
-// `end`: the place of the run's last unit instead of its first one.
-__device__ __forceinline__ Found find_run(const PagedAttn &a, int R, int over, int least, long long *sm, bool end = false) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    const int Bt = a.step.Bt, chunks = (Bt + blockDim.x - 1) / blockDim.x;
-    auto work_of = [&](int b) -> long long {
-        if (b >= Bt) return 0;
-        const Seq s = seq_of(a, b, R);
-        // a context longer than its page-table row: the keys past it do not exist
-        if (s.off + s.n > s.cap) atomicOr(a.status, kDevBadIds);
-        return seq_work(a, s, over);
-    };
+// Every warp finds out for itself (one round of loads and shuffles for up to 32
+// sequences, no barrier).  `end`: the place of the run's last unit instead of
+// its first one.
+__device__ __forceinline__ Found find_run(const PagedAttn &a, int R, int over, int least, bool end = false) {
+    const int lane = threadIdx.x & 31, Bt = a.step.Bt;
     Found f;
-    f.b = 0;
-    f.off = f.work = 0;
-    // one chunk of sequences (the usual case): its work stays in a register;
-    // otherwise a first sweep adds up and a second one searches
-    long long w = work_of(threadIdx.x);
-    for (int c = 1; c < chunks; ++c) w += work_of(c * blockDim.x + threadIdx.x);
-    const long long mine = w;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
-    if (lane == 0) sm[warp] = w;
-    __syncthreads();
-    for (int i = 0; i < nw; ++i) f.work += sm[i];
-    f.run = run_length(f.work, gridDim.x / a.heads, least);
-    f.start = f.run * (blockIdx.x / a.heads);
-    if (f.start >= f.work) return f;
-    const long long u = end ? min(f.start + f.run, f.work) - 1 : f.start;
-    long long base = 0;
-    for (int c = 0; c < chunks; ++c) {
-        const long long x = chunks == 1 ? mine : work_of(c * blockDim.x + threadIdx.x);
-        long long p = x;
+    int work = 0, most = 0, fewest = 0x7FFFFFFF;
+    Seq s = {};
+    int w = 0;
+    for (int b0 = 0; b0 < Bt; b0 += 32) {
+        w = 0;
+        if (b0 + lane < Bt) {
+            s = seq_of(a, b0 + lane, R);
+            w = seq_work(a, s, over);
+            // a context longer than its page-table row: the keys past it do not exist
+            if (s.off + s.n > s.cap) atomicOr(a.status, kDevBadIds);
+            if (w) {
+                most = max(most, s.nk + over);
+                fewest = min(fewest, s.nk + over);
+            }
+        }
+        work += __reduce_add_sync(0xFFFFFFFFu, w);
+    }
+    f.work = work;
+    const int ctas = gridDim.x / a.heads;
+    f.run = max((work + ctas - 1) / ctas, least);
+    // Segments of one size: runs of whole segments, if they are not much longer,
+    // need no merge (which costs about as much as ten tiles).
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    fewest = __reduce_min_sync(0xFFFFFFFFu, fewest);
+    if (most == fewest) {
+        const int whole = (f.run + most - 1) / most * most;
+        if (whole <= f.run + kAlignUnits) f.run = whole;
+    }
+    // (below 2^31 too: whole runs that start inside the work)
+    const int c = blockIdx.x / a.heads;
+    f.start = c <= work / f.run ? c * f.run : work;
+    f.b = f.off = 0;
+    if (f.start >= work) return f;
+    const int u = end ? min(work - f.start, f.run) - 1 + f.start : f.start;
+    int base = 0;
+    for (int b0 = 0; b0 < Bt; b0 += 32) {
+        if (Bt > 32) {
+            w = 0;
+            if (b0 + lane < Bt) {
+                s = seq_of(a, b0 + lane, R);
+                w = seq_work(a, s, over);
+            }
+        }
+        int p = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xFFFFFFFFu, p, o);
+            const int y = __shfl_up_sync(0xFFFFFFFFu, p, o);
             if (lane >= o) p += y;
         }
-        __syncthreads();
-        if (lane == 31) sm[warp] = p;
-        __syncthreads();
-        long long before = base, all = 0;
-        for (int i = 0; i < nw; ++i) {
-            if (i < warp) before += sm[i];
-            all += sm[i];
+        // the first sequence whose end lies behind u
+        const uint32_t behind = __ballot_sync(0xFFFFFFFFu, base + p > u);
+        if (behind) {
+            const int l = __ffs(behind) - 1;
+            f.b = b0 + l;
+            f.off = u - __shfl_sync(0xFFFFFFFFu, base + p - w, l);
+            f.s.cu0 = __shfl_sync(0xFFFFFFFFu, s.cu0, l);
+            f.s.n = __shfl_sync(0xFFFFFFFFu, s.n, l);
+            f.s.off = __shfl_sync(0xFFFFFFFFu, s.off, l);
+            f.s.cap = __shfl_sync(0xFFFFFFFFu, s.cap, l);
+            f.s.nt = __shfl_sync(0xFFFFFFFFu, s.nt, l);
+            f.s.nk = __shfl_sync(0xFFFFFFFFu, s.nk, l);
+            break;
         }
-        const long long first = before + p - x;
-        if (u >= first && u < first + x) {
-            sm[16] = c * static_cast<int>(blockDim.x) + threadIdx.x;
-            sm[17] = u - first;
-        }
-        base += all;
-        if (u < base) break;
+        base += __shfl_sync(0xFFFFFFFFu, p, 31);
     }
-    __syncthreads();
-    f.b = static_cast<int>(sm[16]);
-    f.off = sm[17];
     return f;
 }
 
@@ -175,37 +185,28 @@ __device__ __forceinline__ Found find_run(const PagedAttn &a, int R, int over, i
 struct Walk {
     Seq s;
     int b, rt, h, x0, x1;
-    bool whole;            // all tiles of the segment
-    long long tile0, end0;  // units of the segment's first tile, and behind its last one
-    long long pos, end, off;
-    int over;
-    __device__ __forceinline__ Walk(const Found &f, int over_)
-        : b(f.b), pos(f.start), end(min(f.start + f.run, f.work)), off(f.off), over(over_) {}
+    bool whole;       // all tiles of the segment
+    int tile0, end0;  // units of the segment's first tile, and behind its last one
+    int pos, end, off;
+    int over, hi;     // hi: this CTA's head of those that share the run
+    __device__ __forceinline__ Walk(const PagedAttn &a, const Found &f, int over_)
+        : s(f.s), b(f.b), pos(f.start), end(f.run < f.work - f.start ? f.start + f.run : f.work), off(f.off),
+          over(over_), hi(blockIdx.x % a.heads) {}
     __device__ __forceinline__ bool next(const PagedAttn &a, int R) {
         while (pos < end) {
-            s = seq_of(a, b, R);
             while (off >= seq_work(a, s, over)) {  // (only after a step; bounded by Bt)
                 off = 0;
                 if (++b >= a.step.Bt) return false;
                 s = seq_of(a, b, R);
             }
             const int chunks = a.c.Hkv / a.heads, units = s.nk + over;
-            int seg, u0;  // segment of the sequence, unit of the segment
-            if (off >> 31) {
-                const long long y = off / units;
-                seg = static_cast<int>(y);
-                u0 = static_cast<int>(off - y * units);
-            } else {
-                seg = static_cast<int>(off) / units;
-                u0 = static_cast<int>(off) - seg * units;
-            }
+            const int seg = off / units, u0 = off - seg * units;  // segment of the sequence, unit of it
             const int y = seg / chunks;
-            h = (seg - y * chunks) * a.heads + blockIdx.x % a.heads;
+            h = (seg - y * chunks) * a.heads + hi;
             // last, first, last but one, ...: in a causal chunk late row tiles have more
             // keys than early ones, and a run of several gets its share of both
             rt = y & 1 ? y / 2 : s.nt - 1 - y / 2;
-            const long long left = end - pos;
-            const int u1 = left < units - u0 ? u0 + static_cast<int>(left) : units;
+            const int u1 = min(u0 + end - pos, units);
             tile0 = pos - u0 + over;
             end0 = pos - u0 + units;
             pos += u1 - u0;
@@ -225,8 +226,8 @@ struct Walk {
         return 2ll * blockIdx.x + (tile0 >= f.start ? 1 : 0);
     }
     // First and last run with a piece of the segment.
-    __device__ __forceinline__ int first_run(const Found &f) const { return static_cast<int>(tile0 / f.run); }
-    __device__ __forceinline__ int last_run(const Found &f) const { return static_cast<int>((end0 - 1) / f.run); }
+    __device__ __forceinline__ int first_run(const Found &f) const { return tile0 / f.run; }
+    __device__ __forceinline__ int last_run(const Found &f) const { return (end0 - 1) / f.run; }
 };
 
 // Slot of piece p of a segment that begins in run c0 (its heads' CTAs share it).
