@@ -709,38 +709,38 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
             sums[wg * R + key] = (tops[key] + tops[TW + key]) + (tops[2 * TW + key] + tops[3 * TW + key]);
             if (m != maxima) maxima[key] = maxima[R + key];
         }
-        // the second warpgroup hands over its columns' sums; it then writes the
-        // second half of the rows
-        float *pool = reinterpret_cast<float *>(p_s);
-        static_assert(2 * T::PBYTES >= R * 128 * 4, "exchange buffer");
+        float *pool = reinterpret_cast<float *>(p_s);  // [warpgroup][row][column]
+        static_assert(2 * T::PBYTES >= 2 * R * 128 * 4, "exchange buffer");
 #pragma unroll
-        for (int r = 0; r < R / 2; ++r) pool[(r + wg * (R / 2)) * 128 + key] = wg ? o[r] : o[R / 2 + r];
+        for (int r = 0; r < R; ++r) pool[(wg * R + r) * 128 + key] = o[r];
         named_barrier(1, kCompute);
         const long long prow = walk.slot(found) * R;
-#pragma unroll
-        for (int e = 0; e < R / 2; ++e) {
-            const int r = wg * (R / 2) + e, row = t.r0 + r;
-            if (row >= t.rows) break;
-            const float mine = wg ? o[R / 2 + e] : o[e], other = pool[(e + (wg ^ 1) * (R / 2)) * 128 + key];
-            const float m0 = maxima_s[wg * 2 * R + r], m1 = maxima_s[(wg ^ 1) * 2 * R + r];
-            const float l0 = sums[wg * R + r], l1 = sums[(wg ^ 1) * R + r];
-            const float top = fmaxf(m0, m1);
-            const float f0 = m0 == -INFINITY ? (l0 == 0.f ? 0.f : 1.f) : ex2_approx(m0 - top);
-            const float f1 = m1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : ex2_approx(m1 - top);
+#pragma unroll 1
+        for (int r = warp; r < R && t.r0 + r < t.rows; r += kCompute / 32) {  // a warp per row
+            const float m0 = maxima_s[r], m1 = maxima_s[2 * R + r], l0 = sums[r], l1 = sums[R + r];
+            const float top = fmaxf(m0, m1), z = top == -INFINITY ? 0.f : top;
+            // (a warpgroup without a key has sums 0; NaN sums stay)
+            const float f0 = m0 == -INFINITY ? 1.f : ex2_approx(m0 - z), f1 = m1 == -INFINITY ? 1.f : ex2_approx(m1 - z);
             const float sum = l0 * f0 + l1 * f1;
             float inv = sum == 0.f ? 0.f : 1.f / sum;
             if (I8 && poison[r]) inv = __uint_as_float(0x7FC00000u);
-            const float y = (mine * f0 + other * f1) * inv;
-            const float lse2 = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) + __log2f(sum);
-            if (walk.whole) {
-                const int tok = row / a.G;
-                const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq +
-                                       static_cast<long long>(walk.h) * a.G + (row - tok * a.G);
-                if (key < D) static_cast<__nv_bfloat16 *>(a.out)[orow * D + key] = __float2bfloat16_rn(y);
-                if (key == 0) a.lse[orow] = lse2 * kLn2f;
-            } else {
-                if (key < D) a.part_o[(prow + r) * D + key] = y;
-                if (key == 0) a.part_lse[prow + r] = lse2;
+            const float lse2 = sum == 0.f ? -INFINITY : z + __log2f(sum);
+            const int row = t.r0 + r, tok = row / a.G;
+            const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (row - tok * a.G);
+#pragma unroll
+            for (int c = 2 * lane; c < D; c += 64) {
+                const float2 x = *reinterpret_cast<const float2 *>(pool + r * 128 + c), y = *reinterpret_cast<const float2 *>(pool + (R + r) * 128 + c);
+                const float u = (x.x * f0 + y.x * f1) * inv, v = (x.y * f0 + y.y * f1) * inv;
+                if (walk.whole)
+                    *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + c) = __floats2bfloat162_rn(u, v);
+                else
+                    *reinterpret_cast<float2 *>(a.part_o + (prow + r) * D + c) = make_float2(u, v);
+            }
+            if (lane == 0) {
+                if (walk.whole)
+                    a.lse[orow] = lse2 * kLn2f;
+                else
+                    a.part_lse[prow + r] = lse2;
             }
         }
         if (!walk.whole) {

@@ -388,6 +388,8 @@ def _rows(t: torch.Tensor, device: int, name: str, dims: int) -> int:
         raise ValueError(f"{name} must be a bfloat16 tensor of {dims} dimensions")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, the workspace on cuda:{device}")
+    if t.is_contiguous():
+        return t.shape[1] if dims == 2 else t.shape[1] * t.shape[2]
     shape, stride = t.shape, t.stride()
     width = 1
     for i in range(dims - 1, 0, -1):
@@ -489,12 +491,19 @@ def _gather(fn, dtype, k_pages, v_pages, k_scales, v_scales, page_table, cu, kv_
     Bt, step = _step(page_table, cu, kv_len, num_pages, dev)
     shape = (total, Hkv, d)
     if k is None:
-        k = torch.empty(shape, dtype=_BF16, device=k_pages.device)
+        k = torch.empty(total, Hkv, d, dtype=_BF16, device=k_pages.device)
+        kp = k.data_ptr()
+    elif k.shape != shape:
+        raise ValueError("k must be [total, Hkv, d]")
+    else:
+        kp = _on(k, _BF16, dev, "k")
     if v is None:
         v = torch.empty_like(k)
-    kp, vp = _on(k, _BF16, dev, "k"), _on(v, _BF16, dev, "v")
-    if k.shape != shape or v.shape != shape:
-        raise ValueError("k and v must be [total, Hkv, d]")
+        vp = v.data_ptr()
+    elif v.shape != shape:
+        raise ValueError("v must be [total, Hkv, d]")
+    else:
+        vp = _on(v, _BF16, dev, "v")
     if total:
         _call(fn, ws, stream, *pages, *step, kp, vp, Bt, total, Hkv, d, block)
     return k, v
@@ -519,13 +528,22 @@ def kv_gather_i8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.T
 
 
 def _outputs(q, shape, out, lse, device: int):
+    """out and lse (made here unless given) and their addresses."""
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
+        op = out.data_ptr()
+    elif out.shape != shape:
+        raise ValueError("out shape does not match q")
+    else:
+        op = _on(out, _BF16, device, "out")
     if lse is None:
-        lse = torch.empty(shape[:-1], dtype=_F32, device=q.device)
-    if out.shape != shape or lse.shape != shape[:-1]:
-        raise ValueError("out / lse shapes do not match q")
-    return out, lse, _on(out, _BF16, device, "out"), _on(lse, _F32, device, "lse")
+        lse = torch.empty(*shape[:-1], dtype=_F32, device=q.device)
+        lp = lse.data_ptr()
+    elif lse.shape != shape[:-1]:
+        raise ValueError("lse shape does not match q")
+    else:
+        lp = _on(lse, _F32, device, "lse")
+    return out, lse, op, lp
 
 
 def _attend(fn, dtype, q, k_pages, v_pages, k_scales, v_scales, page_table, cu, kv_len, ws, window,
