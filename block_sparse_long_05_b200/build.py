@@ -1,8 +1,10 @@
-"""Build libmsa.so (the CUDA library behind include/msa.h) for sm_100a.
+"""Build libmsa.so (the CUDA library behind include/msa.h) for sm_100a, and
+_msa_torch.so, the compiled binding of its paged-cache calls.
 
 Run ``python -m block_sparse_long_05_b200.build`` or call ``build()``.  The
-shared object is written next to this file (in-tree), with the CUDA runtime
-linked statically, so it loads on any machine with an NVIDIA driver.
+shared objects are written next to this file (in-tree).  libmsa has the CUDA
+runtime linked statically, so it loads on any machine with an NVIDIA driver;
+the binding belongs to the torch and Python it was built with.
 """
 from __future__ import annotations
 
@@ -10,11 +12,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmsa.so")
+BINDING = os.path.join(HERE, "_msa_torch.so")
+BINDING_SRC = os.path.join(HERE, "csrc_torch", "binding.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -43,7 +48,9 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every .cu under csrc/ into libmsa.so (sm_100a).  Returns the path."""
+    """Compile every .cu under csrc/ into libmsa.so (sm_100a), and the binding.
+    Returns the library's path."""
+    build_binding(force, verbose)
     if not force and not ptxas_info and up_to_date():
         return LIB
     objs = []
@@ -70,6 +77,33 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
     return LIB
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc_torch/binding.cpp into _msa_torch.so.  Returns the path."""
+    header = os.path.join(ROOT, "include", "msa.h")
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in (BINDING_SRC, header, __file__)):
+        return BINDING
+    import torch
+    base = os.path.dirname(torch.__file__)
+    include = [os.path.join(base, "include"),
+               os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"],
+               os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+               os.path.join(ROOT, "include")]
+    tmp = f"{BINDING}.{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f for i in include for f in ("-isystem", i)), BINDING_SRC, "-o", tmp,
+           "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+           "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

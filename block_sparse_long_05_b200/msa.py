@@ -1,4 +1,5 @@
-"""Python binding of libmsa (the C ABI in include/msa.h), by ctypes.
+"""Python binding of libmsa (the C ABI in include/msa.h), by ctypes; the paged-cache
+calls, which are short, through a compiled module (csrc_torch/binding.cpp).
 
 Argument marshalling only: every step of the MSA hot path runs in the CUDA
 kernels behind the C ABI.  torch supplies device memory and the current CUDA
@@ -7,6 +8,7 @@ stream.  If libmsa.so is missing, every call raises: there is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -364,101 +366,29 @@ def sparse_attn_decode_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     return out, lse
 
 
-# The paged-cache calls are short and called once per layer and token, so their
-# binding keeps to few Python operations per tensor: one check each, against
-# the workspace's device, and one flat foreign call.
-_BF16, _I8, _I32, _F32 = torch.bfloat16, torch.int8, torch.int32, torch.float32
+BINDING_PATH = os.path.join(_HERE, "_msa_torch.so")
+_fast = None
 
 
-def _refuse(t: torch.Tensor, dtype, device: int, name: str):
-    _dev(t, dtype, name)
-    raise ValueError(f"{name} is on {t.device}, the workspace on cuda:{device}")
-
-
-def _on(t: torch.Tensor, dtype, device: int, name: str) -> int:
-    """Address of a contiguous tensor of this type on the workspace's device."""
-    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
-        _refuse(t, dtype, device, name)
-    return t.data_ptr()
-
-
-def _rows(t: torch.Tensor, device: int, name: str, dims: int) -> int:
-    """Elements between the rows of a packed bf16 tensor whose rows are contiguous."""
-    if t.dtype is not _BF16 or t.dim() != dims:
-        raise ValueError(f"{name} must be a bfloat16 tensor of {dims} dimensions")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, the workspace on cuda:{device}")
-    if t.is_contiguous():
-        return t.shape[1] if dims == 2 else t.shape[1] * t.shape[2]
-    shape, stride = t.shape, t.stride()
-    width = 1
-    for i in range(dims - 1, 0, -1):
-        if stride[i] != width and shape[i] != 1:
-            raise ValueError(f"{name}: each row must be contiguous")
-        width *= shape[i]
-    return stride[0] if shape[0] > 1 else width
-
-
-def _stores(k_pages, v_pages, k_scales, v_scales, dtype, device: int):
-    """Shape and addresses of a checked pair of page stores (and their scales)."""
-    shape = k_pages.shape
-    if len(shape) != 4 or v_pages.shape != shape:
-        raise ValueError("k_pages and v_pages must be [num_pages, block, Hkv, d]")
-    at = (_on(k_pages, dtype, device, "k_pages"), _on(v_pages, dtype, device, "v_pages"))
-    if dtype is _I8:
-        want = (shape[0], shape[2], shape[1])
-        if k_scales.shape != want or v_scales.shape != want:
-            raise ValueError("k_scales and v_scales must be [num_pages, Hkv, block]")
-        at += (_on(k_scales, _F32, device, "k_scales"), _on(v_scales, _F32, device, "v_scales"))
-    return shape, at
-
-
-def _step(page_table, cu, kv_len, num_pages: int, device: int):
-    """Bt and the arguments page_table, page_stride, num_pages, cu, kv_len."""
-    shape, Bt = page_table.shape, kv_len.shape[0] if kv_len.dim() == 1 else -1
-    if len(shape) != 2 or shape[0] != Bt or cu.shape != (Bt + 1,):
-        raise ValueError("page_table must be [Bt, page_stride], cu [Bt + 1], kv_len [Bt]")
-    return Bt, (_on(page_table, _I32, device, "page_table"), shape[1], num_pages,
-                _on(cu, _I32, device, "cu"), _on(kv_len, _I32, device, "kv_len"))
-
-
-def _call(fn: str, ws: Workspace, stream, *args):
-    """The call on the workspace's device and that device's current stream."""
-    device = ws.device_index
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
-    call = getattr(_lib or load_library(), fn)
-    if torch._C._cuda_getDevice() == device:
-        code = call(*args, ws.ptr, ws.nbytes, stream)
-    else:
-        with torch.cuda.device(device):
-            code = call(*args, ws.ptr, ws.nbytes, stream)
-    if code:
-        raise MSAError(fn, code)
-
-
-def _append(fn, dtype, k, v, k_pages, v_pages, k_scales, v_scales, page_table, cu, kv_len, ws,
-            k_idx, k_idx_pages, stream):
-    dev = ws.device_index
-    (num_pages, block, Hkv, d), pages = _stores(k_pages, v_pages, k_scales, v_scales, dtype, dev)
-    Bt, step = _step(page_table, cu, kv_len, num_pages, dev)
-    ks, vs = _rows(k, dev, "k", 3), _rows(v, dev, "v", 3)
-    total = k.shape[0]
-    if k.shape != (total, Hkv, d) or v.shape != (total, Hkv, d):
-        raise ValueError("k and v must be [total, Hkv, d]")
-    d_idx, xs, xp, xpp = 0, 0, None, None
-    if k_idx is not None or k_idx_pages is not None:
-        if k_idx is None or k_idx_pages is None:
-            raise ValueError("k_idx and k_idx_pages go together")
-        xs, xpp = _rows(k_idx, dev, "k_idx", 2), _on(k_idx_pages, _BF16, dev, "k_idx_pages")
-        xp, d_idx = k_idx.data_ptr(), k_idx.shape[1]
-        if k_idx.shape[0] != total or k_idx_pages.shape != (num_pages, block, d_idx):
-            raise ValueError("k_idx must be [total, d_idx], k_idx_pages [num_pages, block, d_idx]")
-    if total:  # (a step without rows has nothing to write, and no pointers to check)
-        _call(fn, ws, stream, k.data_ptr(), ks, v.data_ptr(), vs, xp, xs, *pages, xpp, *step, Bt,
-              total, Hkv, d, d_idx, block)
+def load_binding(path: str = BINDING_PATH):
+    """Load the compiled binding of the paged-cache calls (raises if it has not been
+    built).  It checks the tensors against the workspace's device, makes the outputs
+    that are not given, and calls libmsa on that device and its current stream."""
+    global _fast
+    if _fast is not None:
+        return _fast
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with "
+                           "`python -m block_sparse_long_05_b200.build`")
+    lib = load_library()
+    spec = importlib.util.spec_from_file_location("_msa_torch", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(getattr(lib, "msa_" + f), ctypes.c_void_p).value for f in (
+        "kv_append", "kv_append_i8", "kv_gather", "kv_gather_i8", "attn_paged", "attn_paged_i8",
+        "sparse_attn_paged_i8")))
+    _fast = mod
+    return mod
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -469,8 +399,11 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: 
     may be strided), k_pages / v_pages [num_pages, block, Hkv, d] bf16, page_table
     [Bt, page_stride], cu [Bt + 1], kv_len [Bt] int32; optionally the index keys k_idx
     [total, d_idx] into k_idx_pages [num_pages, block, d_idx]."""
-    _append("msa_kv_append", _BF16, k, v, k_pages, v_pages, None, None, page_table, cu, kv_len, ws,
-            k_idx, k_idx_pages, stream)
+    r = (_fast or load_binding()).append(ws.ptr, ws.nbytes, ws.device_index, stream, False, k, v,
+                                         k_pages, v_pages, None, None, page_table, cu, kv_len,
+                                         k_idx, k_idx_pages)
+    if r is not None:
+        raise MSAError("msa_kv_append", r)
 
 
 def kv_append_i8(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -480,33 +413,11 @@ def kv_append_i8(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
                  stream=None) -> None:
     """kv_append into int8 pages with a scale per (token, kv head) row
     (msa_kv_append_i8): k_scales / v_scales [num_pages, Hkv, block] fp32."""
-    _append("msa_kv_append_i8", _I8, k, v, k_pages, v_pages, k_scales, v_scales, page_table, cu,
-            kv_len, ws, k_idx, k_idx_pages, stream)
-
-
-def _gather(fn, dtype, k_pages, v_pages, k_scales, v_scales, page_table, cu, kv_len, total, ws, k,
-            v, stream):
-    dev = ws.device_index
-    (num_pages, block, Hkv, d), pages = _stores(k_pages, v_pages, k_scales, v_scales, dtype, dev)
-    Bt, step = _step(page_table, cu, kv_len, num_pages, dev)
-    shape = (total, Hkv, d)
-    if k is None:
-        k = torch.empty(total, Hkv, d, dtype=_BF16, device=k_pages.device)
-        kp = k.data_ptr()
-    elif k.shape != shape:
-        raise ValueError("k must be [total, Hkv, d]")
-    else:
-        kp = _on(k, _BF16, dev, "k")
-    if v is None:
-        v = torch.empty_like(k)
-        vp = v.data_ptr()
-    elif v.shape != shape:
-        raise ValueError("v must be [total, Hkv, d]")
-    else:
-        vp = _on(v, _BF16, dev, "v")
-    if total:
-        _call(fn, ws, stream, *pages, *step, kp, vp, Bt, total, Hkv, d, block)
-    return k, v
+    r = (_fast or load_binding()).append(ws.ptr, ws.nbytes, ws.device_index, stream, True, k, v,
+                                         k_pages, v_pages, k_scales, v_scales, page_table, cu,
+                                         kv_len, k_idx, k_idx_pages)
+    if r is not None:
+        raise MSAError("msa_kv_append_i8", r)
 
 
 def kv_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
@@ -514,8 +425,11 @@ def kv_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Te
               k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
     """Cached rows of a step's positions as packed bf16 (msa_kv_gather):
     -> (k, v) [total, Hkv, d].  Rows behind cu[Bt] are left as they were."""
-    return _gather("msa_kv_gather", _BF16, k_pages, v_pages, None, None, page_table, cu, kv_len,
-                   total, ws, k, v, stream)
+    r = (_fast or load_binding()).gather(ws.ptr, ws.nbytes, ws.device_index, stream, False, total,
+                                         k_pages, v_pages, None, None, page_table, cu, kv_len, k, v)
+    if r.__class__ is int:
+        raise MSAError("msa_kv_gather", r)
+    return r
 
 
 def kv_gather_i8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
@@ -523,43 +437,12 @@ def kv_gather_i8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.T
                  kv_len: torch.Tensor, total: int, ws: Workspace, k: torch.Tensor | None = None,
                  v: torch.Tensor | None = None, stream=None):
     """kv_gather from int8 pages (msa_kv_gather_i8): code * scale, rounded once."""
-    return _gather("msa_kv_gather_i8", _I8, k_pages, v_pages, k_scales, v_scales, page_table, cu,
-                   kv_len, total, ws, k, v, stream)
-
-
-def _outputs(q, shape, out, lse, device: int):
-    """out and lse (made here unless given) and their addresses."""
-    if out is None:
-        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
-        op = out.data_ptr()
-    elif out.shape != shape:
-        raise ValueError("out shape does not match q")
-    else:
-        op = _on(out, _BF16, device, "out")
-    if lse is None:
-        lse = torch.empty(*shape[:-1], dtype=_F32, device=q.device)
-        lp = lse.data_ptr()
-    elif lse.shape != shape[:-1]:
-        raise ValueError("lse shape does not match q")
-    else:
-        lp = _on(lse, _F32, device, "lse")
-    return out, lse, op, lp
-
-
-def _attend(fn, dtype, q, k_pages, v_pages, k_scales, v_scales, page_table, cu, kv_len, ws, window,
-            sinks, max_q, out, lse, stream):
-    dev = ws.device_index
-    (num_pages, block, Hkv, d), pages = _stores(k_pages, v_pages, k_scales, v_scales, dtype, dev)
-    Bt, step = _step(page_table, cu, kv_len, num_pages, dev)
-    q_stride, shape = _rows(q, dev, "q", 3), q.shape
-    total, Hq, d2 = shape
-    if d2 != d:
-        raise ValueError("q must be [total, Hq, d]")
-    out, lse, op, lp = _outputs(q, shape, out, lse, dev)
-    if total:
-        _call(fn, ws, stream, q.data_ptr(), q_stride, *pages, *step, op, lp, Bt, total, max_q or 0,
-              Hq, Hkv, d, block, window, sinks)
-    return out, lse
+    r = (_fast or load_binding()).gather(ws.ptr, ws.nbytes, ws.device_index, stream, True, total,
+                                         k_pages, v_pages, k_scales, v_scales, page_table, cu,
+                                         kv_len, k, v)
+    if r.__class__ is int:
+        raise MSAError("msa_kv_gather_i8", r)
+    return r
 
 
 def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -571,8 +454,12 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     [num_pages, block, Hkv, d] bf16 -> (out [total, Hq, d] bf16, lse [total, Hq] fp32).
     window > 0: each query sees the last `window` keys and the first `sinks` ones.
     max_q: the largest number of rows of one sequence, if known (it chooses kernels)."""
-    return _attend("msa_attn_paged", _BF16, q, k_pages, v_pages, None, None, page_table, cu,
-                   kv_len, ws, window, sinks, max_q, out, lse, stream)
+    r = (_fast or load_binding()).attend(ws.ptr, ws.nbytes, ws.device_index, stream, False, q,
+                                         k_pages, v_pages, None, None, page_table, cu, kv_len,
+                                         window, sinks, max_q, out, lse)
+    if r.__class__ is int:
+        raise MSAError("msa_attn_paged", r)
+    return r
 
 
 def attn_paged_i8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -581,8 +468,12 @@ def attn_paged_i8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                   sinks: int = 0, max_q: int | None = None, out: torch.Tensor | None = None,
                   lse: torch.Tensor | None = None, stream=None):
     """attn_paged over int8 pages with their scales (msa_attn_paged_i8)."""
-    return _attend("msa_attn_paged_i8", _I8, q, k_pages, v_pages, k_scales, v_scales, page_table,
-                   cu, kv_len, ws, window, sinks, max_q, out, lse, stream)
+    r = (_fast or load_binding()).attend(ws.ptr, ws.nbytes, ws.device_index, stream, True, q,
+                                         k_pages, v_pages, k_scales, v_scales, page_table, cu,
+                                         kv_len, window, sinks, max_q, out, lse)
+    if r.__class__ is int:
+        raise MSAError("msa_attn_paged_i8", r)
+    return r
 
 
 def sparse_attn_paged_i8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -592,19 +483,11 @@ def sparse_attn_paged_i8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     """Decode sparse branch over int8 pages (msa_sparse_attn_paged_i8): q [Bt, 1, Hq, d]
     bf16, ids [Bt, 1, K] int32 -> (out [Bt, 1, Hq, d] bf16, lse [Bt, 1, Hq] fp32).  ws is
     a cache workspace (Workspace.for_cache)."""
-    dev = ws.device_index
-    (num_pages, block, Hkv, d), pages = _stores(k_pages, v_pages, k_scales, v_scales, _I8, dev)
-    qp, shape = _on(q, _BF16, dev, "q"), q.shape
-    Bt, n_q, Hq, d2 = shape
-    K = ids.shape[-1]
-    if n_q != 1 or d2 != d or ids.shape != (Bt, 1, K) or page_table.dim() != 2 or \
-            page_table.shape[0] != Bt:
-        raise ValueError("paged attention: shapes do not match")
-    out, lse, op, lp = _outputs(q, shape, out, lse, dev)
-    _call("msa_sparse_attn_paged_i8", ws, stream, qp, *pages,
-          _on(page_table, _I32, dev, "page_table"), page_table.shape[1], num_pages,
-          _on(ids, _I32, dev, "ids"), op, lp, Bt, T, Hq, Hkv, d, block, K)
-    return out, lse
+    r = (_fast or load_binding()).sparse(ws.ptr, ws.nbytes, ws.device_index, stream, q, k_pages,
+                                         v_pages, k_scales, v_scales, page_table, T, ids, out, lse)
+    if r.__class__ is int:
+        raise MSAError("msa_sparse_attn_paged_i8", r)
+    return r
 
 
 def device_status(ws: Workspace, stream=None) -> int:

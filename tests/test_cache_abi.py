@@ -136,38 +136,39 @@ def test_workspace_size(lib):
     assert lib.msa_cache_workspace_size(8, 2, 96) == 0
 
 
-def test_binding_checks():
-    """The binding refuses tensors that are not on the workspace's device, of
-    another type or shape, or not contiguous, before any call."""
+def test_binding_checks(lib):
+    """The compiled binding refuses tensors that are not CUDA tensors, and arguments
+    that are no tensors at all, before any call."""
     from block_sparse_long_05_b200 import msa
 
-    class Ws:  # a workspace on a device that no tensor here is on
-        device_index = 0
+    class Ws:
+        ptr, nbytes, device_index = FAKE, 1 << 30, 0
 
     pages = torch.zeros((4, 32, 2, 64), dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="CUDA"):
-        msa.kv_append(pages[0], pages[0], pages, pages, None, None, None, Ws)
-    with pytest.raises(ValueError, match="CUDA"):
-        msa.attn_paged(pages[0], pages, pages, None, None, None, Ws)
-    with pytest.raises(ValueError, match="num_pages, block, Hkv, d"):
-        msa.attn_paged(pages[0], pages, pages[:3], None, None, None, Ws)
-    # (the checks themselves, with CPU tensors as if they were on the device: get_device() is -1)
-    cpu = -1
-    with pytest.raises(ValueError, match="contiguous"):
-        msa._rows(pages[0].transpose(1, 2), cpu, "q", 3)
-    with pytest.raises(ValueError, match="bfloat16"):
-        msa._rows(pages[0].float(), cpu, "q", 3)
-    with pytest.raises(ValueError, match="workspace"):
-        msa._rows(pages[0], 0, "q", 3)
-    assert msa._rows(pages[0], cpu, "q", 3) == 128
-    assert msa._rows(pages[0, ::4], cpu, "q", 3) == 512
-    scales = torch.zeros((4, 2, 32))
-    codes = pages.to(torch.int8)
-    shape, at = msa._stores(codes, codes, scales, scales, torch.int8, cpu)
-    assert shape == (4, 32, 2, 64) and len(at) == 4
-    with pytest.raises(ValueError, match="Hkv, block"):
-        msa._stores(codes, codes, scales[:, :1], scales, torch.int8, cpu)
-    i = torch.zeros((3, 5), dtype=torch.int32)
-    with pytest.raises(ValueError, match="Bt"):
-        msa._step(i, i[0, :3], i[0, :3], 4, cpu)
-    assert msa._step(i, i[0, :4], i[0, :3], 4, cpu)[0] == 3
+    i = torch.zeros(3, dtype=torch.int32)
+    codes, scales = pages.to(torch.int8), torch.zeros((4, 2, 32))
+    for call in (lambda: msa.kv_append(pages[0], pages[0], pages, pages, i, i, i, Ws),
+                 lambda: msa.kv_append_i8(pages[0], pages[0], codes, codes, scales, scales, i, i, i, Ws),
+                 lambda: msa.kv_gather(pages, pages, i, i, i, 4, Ws),
+                 lambda: msa.kv_gather_i8(codes, codes, scales, scales, i, i, i, 4, Ws),
+                 lambda: msa.attn_paged(pages[0], pages, pages, i, i, i, Ws),
+                 lambda: msa.attn_paged_i8(pages[0], codes, codes, scales, scales, i, i, i, Ws),
+                 lambda: msa.sparse_attn_paged_i8(pages[:1], codes, codes, scales, scales, i, 9, i, Ws)):
+        with pytest.raises(ValueError, match="must be a CUDA tensor"):
+            call()
+    with pytest.raises(ValueError, match="must be a tensor"):
+        msa.attn_paged(pages[0], None, pages, i, i, i, Ws)
+    with pytest.raises(ValueError, match="negative"):
+        msa.kv_gather(pages, pages, i, i, i, -1, Ws)
+    with pytest.raises((ValueError, TypeError)):
+        msa.kv_gather(pages, pages, i, i, i, "4", Ws)
+
+
+def test_binding_fails_loudly_if_missing(tmp_path):
+    from block_sparse_long_05_b200 import msa
+    saved, msa._fast = msa._fast, None
+    try:
+        with pytest.raises(RuntimeError, match="missing"):
+            msa.load_binding(str(tmp_path / "_msa_torch.so"))
+    finally:
+        msa._fast = saved

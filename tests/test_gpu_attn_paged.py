@@ -258,6 +258,33 @@ def test_store_past_32_bits():
     torch.cuda.empty_cache()
 
 
+def test_binding_refusals():
+    """Types, shapes and strides that the binding refuses, before any launch."""
+    from block_sparse_long_05_b200 import msa
+    lib_ready()
+    x = Paged([2], [100], 8, 2, 128, 64, i8=True)
+    ws = msa.Workspace.for_cache(8, 2, 128)
+
+    def attend(**ch):
+        a = dict(q=x.q, kp=x.kp, vp=x.vp, ks=x.ks, vs=x.vs, table=x.table, cu=x.cu, kv_len=x.kv_len)
+        how = {k: ch.pop(k) for k in list(ch) if k in ("out", "lse", "window", "max_q")}
+        a.update(ch)
+        return msa.attn_paged_i8(*a.values(), ws, **how)
+
+    good = attend()
+    for ch in (dict(q=x.q.float()), dict(q=x.q[0]), dict(q=x.q[:, :, :64]), dict(q=x.q.transpose(0, 1)),
+               dict(kp=x.kp.float()), dict(kp=x.kp[:, ::2]), dict(vp=x.vp[1:]), dict(ks=x.ks[:, :1]),
+               dict(vs=x.vs.double()), dict(table=x.table.long()), dict(table=x.table[0]),
+               dict(table=x.table[:, ::2]), dict(cu=x.cu[:1]), dict(kv_len=x.cu), dict(kv_len=x.kv_len.cpu()),
+               dict(out=good[0].float()), dict(out=good[0][:1]), dict(lse=good[1][:, :4]), dict(window=1 << 40)):
+        with pytest.raises(ValueError):
+            attend(**ch)
+    for ch in (dict(window=-1), dict(max_q=-3)):
+        with pytest.raises(msa.MSAError):
+            attend(**ch)
+    assert msa.device_status(ws) == 0
+
+
 # ------------------------------------------------------------------ sparse branch
 @pytest.mark.parametrize("case", [
     # Bt, T, Hq, Hkv, d, block, K
