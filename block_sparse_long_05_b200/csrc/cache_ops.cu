@@ -12,10 +12,16 @@
 //                  as NaN instead of as values that look sound.
 //   gather  packed bf16 rows <- code_i * scale, rounded once (int8), or a copy.
 //
-// Both are bound by HBM: bytes per value are 2 + 1 (int8) or 2 + 2 (bf16).
-// A thread moves 16-byte pieces and issues kPieces loads before it uses any;
-// the page of each token is looked up once per token of the CTA's run, into
-// shared memory, while those loads are in flight.
+// Both are bound by HBM: bytes per value are 2 + 1 (int8) or 2 + 2 (bf16).  To
+// get there they must be lean: at 6.5 TB/s an SM has about four issue slots per
+// 32 values.  A thread moves units of 16 bytes of the store: 8 bf16 values, or
+// 16 codes.  Values become codes and codes values by adding a power of two
+// whose last mantissa bit counts 1, so that no conversion instruction (a quarter
+// of the rate) is needed.  The page of each token is looked up once per token of
+// the CTA's run, into shared memory.  Measured: int8 append of 24573 rows (8
+// heads, d 128) 30 us = 5.0 TB/s, int8 gather of 131072 rows 151 us = 5.4 TB/s;
+// one or four units of codes per thread, or pairs of lanes that read 32 bytes
+// side by side and exchange them in registers, were slower.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,31 +29,61 @@
 
 #include "cache.h"
 #include "msa_common.cuh"
+#include "ptx_sm100.cuh"
 
 namespace msa {
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPieces = 4;                       // 16-byte pieces per thread
-constexpr int kRun = kThreads * kPieces;         // pieces per CTA
-constexpr int kMaxTokens = kRun / 8 + 2;         // tokens that a run touches (>= 8 pieces each)
+template <bool I8>
+struct Units {
+    static constexpr int VALUES = I8 ? 16 : 8;          // of a unit
+    static constexpr int PER = I8 ? 2 : 4;              // units per thread
+    static constexpr int RUN = kThreads * PER;          // units per CTA
+    static constexpr int TOKENS = RUN / (64 / VALUES) + 2;  // tokens that a run touches, at most
+};
 constexpr float kTiny = 7.888609e-31f;           // 2^-100
+constexpr float kMagic = 12582912.f;             // 1.5 * 2^23
+
+// Division of n < 2^31 by a number that the host knows.
+struct Divisor {
+    uint32_t d, mul, shift;
+    explicit Divisor(uint32_t by) : d(by), mul(0), shift(0) {
+        while (shift < 31 && (1u << shift) < by) ++shift;
+        // ceil(2^(31 + shift) / by): exact quotients below 2^31
+        mul = static_cast<uint32_t>(((1ull << (31 + shift)) + by - 1) / by);
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const {
+        return static_cast<uint32_t>((static_cast<uint64_t>(n) * mul) >> 31 >> shift);
+    }
+};
+
+// The step's row offsets in shared memory, unless there are too many: a
+// search for a row's sequence is then a chain of shared-memory reads, not of
+// trips to L2 (which made an append of 24 K rows twice as long).
+constexpr int kSharedSeqs = 1024;
+__device__ __forceinline__ const int32_t *share_offsets(const StepMap &s, int32_t *sh) {
+    if (s.Bt > kSharedSeqs) return s.cu;
+    for (int i = threadIdx.x; i <= s.Bt; i += kThreads) sh[i] = s.cu[i];
+    __syncthreads();
+    return sh;
+}
 
 // Page (x) and row in the page (y) that packed row `tok` maps to.  x = -1:
 // none, the row lies behind the last sequence; -2: none, its position is
 // below 0 or no such page exists (the latter is reported).
-__device__ __forceinline__ int2 store_row(const StepMap &s, int tok, int *status) {
+__device__ __forceinline__ int2 store_row(const StepMap &s, const int32_t *cu, int tok, int *status) {
     int lo = 0, hi = s.Bt;  // first b with cu[b + 1] > tok
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (s.cu[mid + 1] > tok)
+        if (cu[mid + 1] > tok)
             hi = mid;
         else
             lo = mid + 1;
     }
-    if (lo >= s.Bt || tok < s.cu[lo]) return make_int2(-1, 0);
-    const long long pos = static_cast<long long>(s.kv_len[lo]) - s.cu[lo + 1] + tok;
+    if (lo >= s.Bt || tok < cu[lo]) return make_int2(-1, 0);
+    const long long pos = static_cast<long long>(s.kv_len[lo]) - cu[lo + 1] + tok;
     if (pos < 0) return make_int2(-2, 0);
     const long long j = pos / s.block;
     int page = -1;
@@ -67,15 +103,6 @@ __device__ __forceinline__ uint4 ld_once(const void *p) {
     return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-}
-
 struct AppendArgs {
     StepMap step;
     CacheStore c;
@@ -84,84 +111,106 @@ struct AppendArgs {
     __nv_bfloat16 *k_idx_pages;
     int d_idx;
     int kv_ctas;  // CTAs of K and V; those behind them copy index keys
+    Divisor kv_units, idx_units;  // units per token
     int *status;
 };
 
-// PPR: 16-byte pieces per (token, head) row of bf16.  A piece's place in the
-// step is ((token * 2 + {K, V}) * Hkv + head) * PPR + piece, so a warp holds
-// whole rows and reduces amax over PPR lanes.
-template <int PPR, bool I8>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a) {
-    __shared__ int2 dest[kMaxTokens];
+// UPR: units per (token, head) row.  A unit's place in the step is
+// ((token * 2 + {K, V}) * Hkv + head) * UPR + unit, so a warp holds whole rows
+// and reduces amax over UPR lanes.
+template <int UPR, bool I8>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+    using U = Units<I8>;
+    __shared__ int2 dest[U::TOKENS];
+    __shared__ int32_t offsets[kSharedSeqs + 1];
     const int tid = threadIdx.x;
     const bool index = static_cast<int>(blockIdx.x) >= a.kv_ctas;
-    // (the host keeps the number of pieces below 2^31)
-    const uint32_t run = (blockIdx.x - (index ? a.kv_ctas : 0)) * kRun;
-    const uint32_t ppt = index ? a.d_idx / 8 : 2 * a.c.Hkv * PPR;  // pieces per token
-    const uint32_t total = a.step.total * ppt;
-    const int tok0 = static_cast<int>(run / ppt);
-    const int ntok = static_cast<int>((min(run + kRun, total) - 1) / ppt) - tok0 + 1;
-    uint4 x[kPieces];
-    int tok[kPieces], rem[kPieces];
+    // (the host keeps the number of units below 2^31)
+    const uint32_t run = (blockIdx.x - (index ? a.kv_ctas : 0)) * U::RUN;
+    const Divisor &upt = index ? a.idx_units : a.kv_units;
+    const uint32_t total = a.step.total * upt.d, half = a.c.Hkv * UPR;
+    const int tok0 = static_cast<int>(upt.quotient(run));
+    const int ntok = static_cast<int>(upt.quotient(min(run + U::RUN, total) - 1)) - tok0 + 1;
+    uint4 x[U::PER][I8 ? 2 : 1];
+    int tok[U::PER];
+    uint32_t unit[U::PER];
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < U::PER; ++i) {
         const uint32_t e = run + i * kThreads + tid;
         tok[i] = -1;
-        rem[i] = 0;
-        x[i] = make_uint4(0, 0, 0, 0);
+        unit[i] = 0;
+#pragma unroll
+        for (int k = 0; k < (I8 ? 2 : 1); ++k) x[i][k] = make_uint4(0, 0, 0, 0);
         if (e >= total) continue;
-        tok[i] = static_cast<int>(e / ppt);
-        rem[i] = static_cast<int>(e % ppt);
-        if (index) {
-            x[i] = ld_once(a.k_idx + tok[i] * a.k_idx_stride + rem[i] * 8);
-        } else {
-            const int half = a.c.Hkv * PPR;
-            x[i] = rem[i] < half ? ld_once(a.k + tok[i] * a.k_stride + rem[i] * 8)
-                                 : ld_once(a.v + tok[i] * a.v_stride + (rem[i] - half) * 8);
-        }
+        tok[i] = static_cast<int>(upt.quotient(e));
+        unit[i] = e - tok[i] * upt.d;
+        const __nv_bfloat16 *src;
+        if (index)
+            src = a.k_idx + tok[i] * a.k_idx_stride + unit[i] * U::VALUES;
+        else if (unit[i] < half)
+            src = a.k + tok[i] * a.k_stride + unit[i] * U::VALUES;
+        else
+            src = a.v + tok[i] * a.v_stride + (unit[i] - half) * U::VALUES;
+        x[i][0] = ld_once(src);
+        if (I8) x[i][I8] = ld_once(src + 8);
     }
-    for (int t = tid; t < ntok; t += kThreads) dest[t] = store_row(a.step, tok0 + t, a.status);
+    const int32_t *cu = share_offsets(a.step, offsets);
+    for (int t = tid; t < ntok; t += kThreads) dest[t] = store_row(a.step, cu, tok0 + t, a.status);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < U::PER; ++i) {
         const int2 to = tok[i] >= 0 ? dest[tok[i] - tok0] : make_int2(-1, 0);
         const bool keep = to.x >= 0;
         const long long row = static_cast<long long>(to.x) * a.step.block + to.y;
         if (index) {
-            if (keep)
-                *reinterpret_cast<uint4 *>(a.k_idx_pages + row * a.d_idx + rem[i] * 8) = x[i];
+            if (keep) {
+                uint4 *out = reinterpret_cast<uint4 *>(a.k_idx_pages + row * a.d_idx + unit[i] * U::VALUES);
+                out[0] = x[i][0];
+                if (I8) out[1] = x[i][I8];
+            }
             continue;
         }
-        const int half = a.c.Hkv * PPR;
-        const bool is_v = rem[i] >= half;
-        const int hp = is_v ? rem[i] - half : rem[i];  // head * PPR + piece
+        const bool is_v = unit[i] >= half;
+        const uint32_t hu = is_v ? unit[i] - half : unit[i];  // head * UPR + unit
         void *pages = is_v ? a.c.v : a.c.k;
         if (!I8) {
-            if (keep) reinterpret_cast<uint4 *>(pages)[row * half + hp] = x[i];
+            if (keep) reinterpret_cast<uint4 *>(pages)[row * half + hu] = x[i][0];
             continue;
         }
+        const uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][I8].x, x[i][I8].y, x[i][I8].z, x[i][I8].w};
         // |x| as 15-bit patterns order like the values, infinities and NaN on top
-        uint32_t m = __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
-                              __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
+        uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-        for (int o = 1; o < PPR; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        for (int e = 1; e < 8; ++e) m = __vmaxu2(m, w[e] & 0x7FFF7FFFu);
+#pragma unroll
+        for (int o = 1; o < UPR; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         const uint32_t top = max(m & 0xFFFFu, m >> 16) << 16;
         const float amax = __uint_as_float(top);
         const bool bad = top >= 0x7F800000u, tiny = amax < kTiny;
         const float inv = bad || tiny ? 0.f : __fdiv_rn(127.f, amax);
-        float f[8];
-        unpack8(x[i], f);
-        uint32_t w[2] = {0, 0};
-        if (!bad) {
+        const uint64_t magic2 = f2_pack(kMagic, kMagic);
+        uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                w[e / 4] |= (static_cast<uint32_t>(__float2int_rn(f[e] * inv)) & 0xFFu) << (8 * (e % 4));
+        for (int e = 0; e < 4; ++e) {
+            // (product and sum rounded one by one: rint(x * inv), as documented; packed
+            // products were fused into the sums)
+            uint32_t y[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t u = w[2 * e + k];
+                float f0, f1;
+                f2_unpack(f2_add(f2_pack(__fmul_rn(__uint_as_float(u << 16), inv), __fmul_rn(__uint_as_float(u & 0xFFFF0000u), inv)), magic2), f0, f1);
+                y[2 * k] = __float_as_uint(f0);
+                y[2 * k + 1] = __float_as_uint(f1);
+            }
+            o[e] = __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
+            if (bad) o[e] = 0;
         }
         if (keep) {
-            reinterpret_cast<uint2 *>(pages)[row * half + hp] = make_uint2(w[0], w[1]);
-            if (hp % PPR == 0) {
+            reinterpret_cast<uint4 *>(pages)[row * half + hu] = make_uint4(o[0], o[1], o[2], o[3]);
+            if (hu % UPR == 0) {
                 float *scales = is_v ? a.c.v_scales : a.c.k_scales;
-                scales[(static_cast<long long>(to.x) * a.c.Hkv + hp / PPR) * a.step.block + to.y] =
+                scales[(static_cast<long long>(to.x) * a.c.Hkv + hu / UPR) * a.step.block + to.y] =
                     bad ? __uint_as_float(0x7FC00000u) : tiny ? 0.f : __fdiv_rn(amax, 127.f);
             }
         }
@@ -172,6 +221,7 @@ struct GatherArgs {
     StepMap step;
     CacheStore c;
     void *k_out, *v_out;
+    Divisor units;  // per token
     int *status;
 };
 
@@ -180,57 +230,59 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// PPR: 16-byte pieces per cached (token, head) row.
-template <int PPR, bool I8>
-__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a) {
-    __shared__ int2 src[kMaxTokens];
+template <int UPR, bool I8>
+__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const __grid_constant__ GatherArgs a) {
+    using U = Units<I8>;
+    __shared__ int2 src[U::TOKENS];
+    __shared__ int32_t offsets[kSharedSeqs + 1];
     const int tid = threadIdx.x;
-    const uint32_t half = a.c.Hkv * PPR, ppt = 2 * half;
-    const uint32_t run = blockIdx.x * kRun;  // (the host keeps the number of pieces below 2^31)
-    const uint32_t total = a.step.total * ppt;
-    const int tok0 = static_cast<int>(run / ppt);
-    const int ntok = static_cast<int>((min(run + kRun, total) - 1) / ppt) - tok0 + 1;
-    for (int t = tid; t < ntok; t += kThreads) src[t] = store_row(a.step, tok0 + t, a.status);
+    const uint32_t half = a.c.Hkv * UPR;
+    const uint32_t run = blockIdx.x * U::RUN;  // (the host keeps the number of units below 2^31)
+    const uint32_t total = a.step.total * a.units.d;
+    const int tok0 = static_cast<int>(a.units.quotient(run));
+    const int ntok = static_cast<int>(a.units.quotient(min(run + U::RUN, total) - 1)) - tok0 + 1;
+    const int32_t *cu = share_offsets(a.step, offsets);
+    for (int t = tid; t < ntok; t += kThreads) src[t] = store_row(a.step, cu, tok0 + t, a.status);
     __syncthreads();
-    uint4 x[kPieces];
-    float s[kPieces];
-    uint4 *to[kPieces];  // nullptr: not written
+    uint4 x[U::PER];
+    float s[U::PER];
+    uint4 *to[U::PER];  // nullptr: not written
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < U::PER; ++i) {
         const uint32_t e = run + i * kThreads + tid;
         x[i] = make_uint4(0, 0, 0, 0);
         s[i] = 0.f;
         to[i] = nullptr;
         if (e >= total) continue;
-        const uint32_t tok = e / ppt, rem = e % ppt;
+        const uint32_t tok = a.units.quotient(e), unit = e - tok * a.units.d;
         const int2 from = src[tok - tok0];
         if (from.x == -1) continue;  // behind the last sequence: left as it is
-        const bool is_v = rem >= half;
-        const uint32_t hp = is_v ? rem - half : rem;  // head * PPR + piece
-        to[i] = reinterpret_cast<uint4 *>(is_v ? a.v_out : a.k_out) +
-                (static_cast<long long>(tok) * half + hp) * (I8 ? 2 : 1);
+        const bool is_v = unit >= half;
+        const uint32_t hu = is_v ? unit - half : unit;  // head * UPR + unit
+        to[i] = reinterpret_cast<uint4 *>(is_v ? a.v_out : a.k_out) + (static_cast<long long>(tok) * half + hu) * (I8 ? 2 : 1);
         if (from.x < 0) continue;  // no such position or page: zeros
         const long long row = static_cast<long long>(from.x) * a.step.block + from.y;
-        x[i] = ld_once(reinterpret_cast<const uint4 *>(is_v ? a.c.v : a.c.k) + row * half + hp);
+        x[i] = ld_once(reinterpret_cast<const uint4 *>(is_v ? a.c.v : a.c.k) + row * half + hu);
         if (I8)
-            s[i] = (is_v ? a.c.v_scales : a.c.k_scales)
-                [(static_cast<long long>(from.x) * a.c.Hkv + hp / PPR) * a.step.block + from.y];
+            s[i] = __ldg((is_v ? a.c.v_scales : a.c.k_scales) +
+                         (static_cast<long long>(from.x) * a.c.Hkv + hu / UPR) * a.step.block + from.y);
     }
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < U::PER; ++i) {
         if (!to[i]) continue;
         if (!I8) {
             *to[i] = x[i];
             continue;
         }
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        const uint64_t s2 = f2_pack(s[i], s[i]), back = f2_pack(-8388736.f, -8388736.f);
         uint32_t o[8];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+            const uint32_t u = w[q] ^ 0x80808080u;  // code + 128, then 2^23 + that as a float
             float f[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                f[b] = static_cast<float>(static_cast<int8_t>(w[q] >> (8 * b))) * s[i];
+            f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540)), __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7541))), back), s2), f[0], f[1]);
+            f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7542)), __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7543))), back), s2), f[2], f[3]);
             o[2 * q] = pack2(f[0], f[1]);
             o[2 * q + 1] = pack2(f[2], f[3]);
         }
@@ -239,7 +291,33 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a)
     }
 }
 
-unsigned runs(long long pieces) { return static_cast<unsigned>((pieces + kRun - 1) / kRun); }
+template <bool I8>
+unsigned runs(long long units) {
+    return static_cast<unsigned>((units + Units<I8>::RUN - 1) / Units<I8>::RUN);
+}
+
+template <int UPR, bool I8>
+cudaError_t run_append(AppendArgs a, int d, cudaStream_t st) {
+    constexpr int V = Units<I8>::VALUES;
+    const int units = 2 * a.c.Hkv * (d / V);
+    a.kv_units = Divisor(units);
+    a.kv_ctas = static_cast<int>(runs<I8>(static_cast<long long>(a.step.total) * units));
+    unsigned grid = a.kv_ctas;
+    if (a.d_idx) {
+        a.idx_units = Divisor(a.d_idx / V);
+        grid += runs<I8>(static_cast<long long>(a.step.total) * (a.d_idx / V));
+    }
+    kv_append_kernel<UPR, I8><<<grid, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int UPR, bool I8>
+cudaError_t run_gather(GatherArgs a, int d, cudaStream_t st) {
+    const int units = 2 * a.c.Hkv * (d / Units<I8>::VALUES);
+    a.units = Divisor(units);
+    kv_gather_kernel<UPR, I8><<<runs<I8>(static_cast<long long>(a.step.total) * units), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
 
 }  // namespace
 
@@ -247,48 +325,18 @@ cudaError_t launch_kv_append(const StepMap &step, const CacheStore &c, const voi
                              long long k_stride, const void *v, long long v_stride,
                              const void *k_idx, long long k_idx_stride, void *k_idx_pages,
                              int d_idx, int *status, cudaStream_t st) {
-    AppendArgs a;
-    a.step = step;
-    a.c = c;
-    a.k = static_cast<const __nv_bfloat16 *>(k);
-    a.v = static_cast<const __nv_bfloat16 *>(v);
-    a.k_idx = static_cast<const __nv_bfloat16 *>(k_idx);
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.k_idx_stride = k_idx_stride;
-    a.k_idx_pages = static_cast<__nv_bfloat16 *>(k_idx_pages);
-    a.d_idx = d_idx;
-    a.status = status;
-    a.kv_ctas = static_cast<int>(runs(static_cast<long long>(step.total) * 2 * c.Hkv * (c.d / 8)));
-    const unsigned grid = a.kv_ctas + (d_idx ? runs(static_cast<long long>(step.total) * (d_idx / 8)) : 0u);
-    if (c.d == 128) {
-        if (c.k_scales) kv_append_kernel<16, true><<<grid, kThreads, 0, st>>>(a);
-        else kv_append_kernel<16, false><<<grid, kThreads, 0, st>>>(a);
-    } else {
-        if (c.k_scales) kv_append_kernel<8, true><<<grid, kThreads, 0, st>>>(a);
-        else kv_append_kernel<8, false><<<grid, kThreads, 0, st>>>(a);
-    }
-    return cudaGetLastError();
+    const AppendArgs a{step, c, static_cast<const __nv_bfloat16 *>(k), static_cast<const __nv_bfloat16 *>(v),
+                       static_cast<const __nv_bfloat16 *>(k_idx), k_stride, v_stride, k_idx_stride,
+                       static_cast<__nv_bfloat16 *>(k_idx_pages), d_idx, 0, Divisor(1), Divisor(1), status};
+    if (c.d == 128) return c.k_scales ? run_append<8, true>(a, 128, st) : run_append<16, false>(a, 128, st);
+    return c.k_scales ? run_append<4, true>(a, 64, st) : run_append<8, false>(a, 64, st);
 }
 
 cudaError_t launch_kv_gather(const StepMap &step, const CacheStore &c, void *k_out, void *v_out,
                              int *status, cudaStream_t st) {
-    GatherArgs a;
-    a.step = step;
-    a.c = c;
-    a.k_out = k_out;
-    a.v_out = v_out;
-    a.status = status;
-    const int ppr = c.d * (c.k_scales ? 1 : 2) / 16;
-    const unsigned grid = runs(static_cast<long long>(step.total) * 2 * c.Hkv * ppr);
-    if (c.k_scales) {
-        if (c.d == 128) kv_gather_kernel<8, true><<<grid, kThreads, 0, st>>>(a);
-        else kv_gather_kernel<4, true><<<grid, kThreads, 0, st>>>(a);
-    } else {
-        if (c.d == 128) kv_gather_kernel<16, false><<<grid, kThreads, 0, st>>>(a);
-        else kv_gather_kernel<8, false><<<grid, kThreads, 0, st>>>(a);
-    }
-    return cudaGetLastError();
+    const GatherArgs a{step, c, k_out, v_out, Divisor(1), status};
+    if (c.d == 128) return c.k_scales ? run_gather<8, true>(a, 128, st) : run_gather<16, false>(a, 128, st);
+    return c.k_scales ? run_gather<4, true>(a, 64, st) : run_gather<8, false>(a, 64, st);
 }
 
 }  // namespace msa
