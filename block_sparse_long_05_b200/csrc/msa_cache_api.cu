@@ -188,16 +188,26 @@ msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int nu
     const long long mean = (static_cast<long long>(a.step.total) + a.step.Bt - 1) / a.step.Bt;
     const long long most = (max_q > mean ? max_q : mean) * a.G;
     const int rows = most <= kSplitMaxRows ? static_cast<int>(most) : kSplitMaxRows + 1;
-    // work units are numbered with 31 bits: row tiles x head groups x key tiles
+    // the most row tiles and key tiles that the step may have
     const long long all = static_cast<long long>(a.step.total) * a.G;
-    const long long tiles = a.ids || rows <= kSplitMaxRows ? all / 8 + a.step.Bt : all / 256 + 2 * a.step.Bt;
-    const long long keys = a.ids ? static_cast<long long>(a.K) * a.step.block : static_cast<long long>(a.step.pm.stride) * a.step.block;
-    if (tiles * (a.c.Hkv / a.heads) * (keys / kSplitKeys + 8) >= (1ll << 31)) return MSA_ERR_UNSUPPORTED;
-    // the chunk kernel for the sequences with many rows, then (if there may be
-    // such) the split kernel for those with few; a hint that is too low costs
-    // time, not rows
+    const long long span = a.ids ? static_cast<long long>(a.K) * a.step.block
+                                 : static_cast<long long>(a.step.pm.stride) * a.step.block;
+    long long keys = span / kSplitKeys + 1;
+    const long long near = (static_cast<long long>(a.window) + a.sinks) / kSplitKeys + 4;
+    if (a.window && keys > near) keys = near;
+    const long long tiles = all / kSplitMaxRows + a.step.Bt;
+    // Sequences with many rows go to the chunk kernel, unless the whole step is
+    // small: it takes 14 us or more where the split kernel, 16 rows at a time, has
+    // done with a few hundred tiles.  Measured (bf16, d 128, G 4; split against
+    // chunk): 64 rows over 500 keys, 8 kv heads: 14 / 23 us; 20 over 2000: 26 / 27;
+    // 200 over 200: 21 / 20; 500 over 500, 2 kv heads: 18 / 24, 8 kv heads:
+    // 53 / 25; 64 over 4000: 45 / 38.  In a batch the split kernel then takes the
+    // sequences with few rows; a hint that is too low costs time, not rows.
+    const bool chunk = rows > kSplitMaxRows && !a.ids && tiles * a.c.Hkv * (keys + 2) > 1536;
+    // work units are numbered with 31 bits
+    const long long row_tiles = chunk ? all / kChunkRows + 2ll * a.step.Bt : 2 * tiles;
+    if (row_tiles * (a.c.Hkv / a.heads) * (keys + 8) >= (1ll << 31)) return MSA_ERR_UNSUPPORTED;
     cudaError_t e = cudaSuccess;
-    const bool chunk = rows > kSplitMaxRows && !a.ids;
     if (chunk) {
         a.row_lo = a.step.Bt > 1 ? kSplitMaxRows + 1 : 0;
         e = launch_chunk_attn(a, tk, tv, sms, st);
@@ -241,7 +251,7 @@ msa_status attn_impl(const void *q, int64_t q_stride, const void *k_pages, const
     a.G = Hq / Hkv;
     // positions stay below 2^30, so a longer window hides nothing
     a.window = window < (1 << 30) ? window : 1 << 30;
-    a.sinks = window ? sinks : 0;
+    a.sinks = !window ? 0 : sinks < (1 << 30) ? sinks : 1 << 30;
     return attend(a, k_pages, v_pages, num_pages, max_q > 0 && max_q < total ? max_q : total, ws, stream);
 }
 

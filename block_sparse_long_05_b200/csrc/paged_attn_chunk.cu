@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                             continue;
                         }
                         const int p = pos + i * 32;
-                        if (p > t.tmax || p >= walk.s.cap) continue;
+                        // (keys before every row's window: their page may be gone)
+                        if (p >= hi || (p + box <= lo && p >= a.sinks)) continue;
                         const int j = p / block;
                         const int page = a.step.pm.table[static_cast<long long>(walk.b) * a.step.pm.stride + j];
                         if (page < 0 || page >= a.step.pm.count) {

@@ -338,7 +338,10 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                             if (p >= a.T) p = -1;
                         } else {
                             p = (x < t.na ? x : x + t.skip) * kKeys + i * 32;
-                            if (p > t.tmax || p >= walk.s.cap) p = -1;
+                            // (keys before every row's window: their page may be gone)
+                            if (p > t.tmax || p >= walk.s.cap ||
+                                (a.window && p + box <= t.tmin - a.window + 1 && p >= a.sinks))
+                                p = -1;
                         }
                         if (p < 0) continue;
                         const int j = p / block;

@@ -174,6 +174,91 @@ def test_dead_rows_of_shared_tiles():
         cache_ref.check(out[:, h], lse[:, h], o, l, *cache_ref.tolerances(o, l, a, s, 128))
 
 
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("n", [1, 3, 100, 600])
+@pytest.mark.parametrize("block", [32, 64, 128])
+def test_pages_before_the_window_may_be_gone(n, i8, block):
+    """A page with no key in any row's window (nor a sink) is not looked up."""
+    window, sinks, T = 150, 5, 1500
+    x = Paged([n], [T], 8, 2, 128, block, i8=i8)
+    first = T - n - window + 1  # the first key that the first row sees
+    for j in range(1 + (sinks - 1) // block, max(first, 0) // block):
+        x.table[0, j] = -1 if j % 2 else x.num_pages + 7
+    keep = x.table.clone()
+    good = Paged([n], [T], 8, 2, 128, block, i8=i8)
+    x.table = good.table
+    want = cache_ref.attn(x, window, sinks)
+    x.table = keep
+    from block_sparse_long_05_b200 import msa
+    lib_ready()
+    ws = msa.Workspace.for_cache(8, 2, 128)
+    out, lse = _run(x, ws, window=window, sinks=sinks)
+    assert msa.device_status(ws) == 0
+    cache_ref.check(out, lse, *want)
+
+
+@pytest.mark.parametrize("n", [1, 6, 300])
+def test_rows_without_sound_scales(n):
+    """A cached row that was not finite when it was written (scale NaN) reaches the
+    queries that see it, and no others; a bad V row leaves lse as it is."""
+    from block_sparse_long_05_b200 import msa
+    lib_ready()
+    T, j = 700, 650 if n > 100 else 700 - (n + 1) // 2
+    for bad in ("v", "k"):
+        x = Paged([n], [T], 8, 2, 128, 64, i8=True)
+        want = cache_ref.attn(x)
+        getattr(x, bad + "s")[int(x.table[0, j // 64]), :, j % 64] = float("nan")
+        ws = msa.Workspace.for_cache(8, 2, 128)
+        out, lse = _run(x, ws)
+        assert msa.device_status(ws) == 0
+        sees = torch.arange(T - n, T, device="cuda") >= j
+        assert torch.isnan(out[sees]).all()
+        if (~sees).any():
+            cache_ref.check(out[~sees], lse[~sees], *(t[~sees] for t in want))
+        if bad == "v":
+            assert ((lse - want[1]).abs() <= want[3]).all()
+        else:
+            assert torch.isnan(lse[sees]).all()
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("n", [2, 300])
+def test_keys_of_later_tokens_may_be_anything(n, i8):
+    """K of a token that a query may not see has no influence, whatever it holds."""
+    from block_sparse_long_05_b200 import msa
+    lib_ready()
+    x = Paged([n], [500], 8, 2, 128, 64, i8=i8)
+    want = cache_ref.attn(x)
+    p, r = int(x.table[0, 499 // 64]), 499 % 64
+    if i8:
+        x.ks[p, :, r] = float("inf")
+    else:
+        x.kp[p, r] = float("nan")
+    ws = msa.Workspace.for_cache(8, 2, 128)
+    out, lse = _run(x, ws)
+    cache_ref.check(out[:-1], lse[:-1], *(t[:-1] for t in want))
+
+
+@pytest.mark.parametrize("i8", [False, True])
+def test_scores_that_leap(i8):
+    """Scores that rise by hundreds from one key tile to the next: the weights'
+    reference is raised again and again, in every row apart."""
+    x = Paged([1, 300], [1400, 1400], 8, 2, 128, 128, i8=i8, scale=0.0)
+    g = torch.Generator().manual_seed(9)
+    for b in range(2):
+        grow = torch.linspace(0, 60, 1400)[:, None, None]
+        k = (torch.randn((1400, 2, 128), generator=g) * grow).to(torch.bfloat16)
+        for j in range(-(-1400 // 128)):
+            lo, hi = j * 128, min((j + 1) * 128, 1400)
+            p = int(x.table[b, j])
+            if i8:
+                codes, sc = cache_ref.quantise(k[lo:hi])
+                x.kp[p, :hi - lo], x.ks[p, :, :hi - lo] = codes.cuda(), sc.t().cuda()
+            else:
+                x.kp[p, :hi - lo] = k[lo:hi].cuda()
+    _both(x)
+
+
 def test_repeats_bit_for_bit():
     from block_sparse_long_05_b200 import msa
     lib_ready()
