@@ -12,7 +12,7 @@
 // thread has a whole row of S in registers: no shuffles.  The running
 // reference m is raised, and O rescaled, only when a score passes it by 2^8.
 //
-// int8 pages: four warps turn the codes into bf16 tiles (exact) ahead of the
+// int8 pages: eight warps turn the codes into bf16 tiles (exact) ahead of the
 // products; the scales sk multiply the scores and sv the weights in fp32.
 //
 // P is rounded to bf16 (a relative error of at most 2^-8 per weight, averaged
@@ -51,13 +51,13 @@ struct Chunk {
     static constexpr int RAW = 128 * D;            // tile of codes
     static constexpr int STAGES = I8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);  // bf16 tiles of K or V
     static constexpr int RAWS = I8 ? (D == 128 ? 3 : 4) : 0;                     // tiles of codes
-    // warps 0-15: softmax; 16-19: int8 conversion; then a producer and a product
+    // warps 0-15: softmax; 16-23: int8 conversion; then a producer and a product
     // warp, and two that fill up their warpgroup.  Registers per thread: at launch
     // THREADS * LAUNCH of the SM's 65536, then split anew.
-    static constexpr int CONV = I8 ? 4 : 0;
-    static constexpr int THREADS = I8 ? 768 : 640;
-    static constexpr int LAUNCH = I8 ? 80 : 96;
-    static constexpr int REST = I8 ? 48 : 64;
+    static constexpr int CONV = I8 ? 8 : 0;
+    static constexpr int THREADS = I8 ? 896 : 640;
+    static constexpr int LAUNCH = I8 ? 72 : 96;
+    static constexpr int REST = I8 ? 40 : 64;
     static constexpr int SOFTMAX = I8 ? 96 : 104;
     static_assert(512 * SOFTMAX + (THREADS - 512) * REST <= THREADS * LAUNCH && THREADS * LAUNCH <= 65536, "registers");
 };
@@ -139,12 +139,12 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     if (tid == 0) {
         for (int i = 0; i < kMetaSlots; ++i) mbar_init(meta_full + i, I8 ? 128 : 1);
         for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(full + i, I8 ? 128 : 1);
+            mbar_init(full + i, I8 ? 256 : 1);
             mbar_init(empty + i, 1);
         }
         for (int i = 0; i < C::RAWS; ++i) {
             mbar_init(raw_full + i, 1);
-            mbar_init(raw_empty + i, 128);
+            mbar_init(raw_empty + i, 256);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_s + i, 1);
@@ -175,9 +175,9 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     if (I8 && warp < kProducer) {
         fewer_registers<C::REST>();
         // -------------------------------------------------------- int8 -> bf16
-        // Thread: one row of the tile; rows of 16-byte pieces, swizzled on both
+        // Thread: half a row of the tile; rows of 16-byte pieces, swizzled on both
         // sides so that eight neighbouring rows fall on different banks.
-        const int r = tid & 127;
+        const int r = tid & 127, half = warp >> 2 & 1;
         uint32_t e = 0, slot = 0;
         bool ok = true;
         auto convert = [&](bool is_v) {
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
             if (!ok) return;
             const unsigned char *src = raw + rs * C::RAW;
             unsigned char *dst = ring + st * C::TILE;
-            if (!is_v) {
+            if (!is_v && half == 0) {
                 float *sc = scales + slot % kMetaSlots * 256;
                 sc[r] = raw_sc[rs * 256 + r];
                 sc[128 + r] = raw_sc[rs * 256 + 128 + r];
@@ -196,15 +196,16 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                 ++slot;
             }
 #pragma unroll
-            for (int p = 0; p < D / 16; ++p) {
+            for (int i = 0; i < D / 32; ++i) {
+                const int p = half * (D / 32) + i;
                 const uint32_t at = D == 128 ? sw128_offset(r, p) : r * 64u + ((p ^ ((r >> 1) & 3u)) << 4);
                 const uint4 u = *reinterpret_cast<const uint4 *>(src + at);
                 const uint32_t w[4] = {u.x, u.y, u.z, u.w};
                 uint32_t o[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    o[2 * i] = s8x2_bf16(__byte_perm(w[i], 0, 0x1100));
-                    o[2 * i + 1] = s8x2_bf16(__byte_perm(w[i], 0, 0x3322));
+                for (int k = 0; k < 4; ++k) {
+                    o[2 * k] = s8x2_bf16(__byte_perm(w[k], 0, 0x1100));
+                    o[2 * k + 1] = s8x2_bf16(__byte_perm(w[k], 0, 0x3322));
                 }
                 unsigned char *to = dst + p / 4 * 16384;
                 *reinterpret_cast<uint4 *>(to + sw128_offset(r, p % 4 * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
