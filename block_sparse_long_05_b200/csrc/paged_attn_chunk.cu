@@ -377,8 +377,9 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                 const RowTile rt = row_tile(a, walk.s, walk.rt, kRows);
                 const int n = min(walk.x1, rt.count) - walk.x0;
                 const int tiles = rt.rows - rt.r0 > 128 ? 2 : 1;
+                if (n <= 0) continue;
                 for (int t = 0; t < tiles && ok; ++t) ok = mbar_wait(q_ready + t, nq[t]++ & 1, abort_flag, a.status);
-                if (!ok || n <= 0) continue;
+                if (!ok) break;
                 uint32_t st = e % C::STAGES;
                 if (!(ok = mbar_wait(full + st, (e / C::STAGES) & 1, abort_flag, a.status))) break;
                 tc_fence_after();
@@ -432,31 +433,36 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     const float *other_x = halves + (t * 2 + (half ^ 1)) * 128 + row;
     uint32_t slot = 0, n_s = 0;  // key tiles; products awaited
     bool ok = true;
-    while (walk.next(a, kRows)) {
+    // Q rows of the segment's tile into shared memory, if the segment has keys
+    auto load_q = [&]() {
         const RowTile rt = row_tile(a, walk.s, walk.rt, kRows);
-        const int x1 = min(walk.x1, rt.count);
+        const int first = rt.r0 + t * 128;
+        if ((t == 1 && rt.rows <= first) || min(walk.x1, rt.count) <= walk.x0) return;
+        constexpr int PPR = D / 8, STEP = 256 / PPR;
+        const int c = row % PPR, r0 = (row + half * 128) / PPR;
+        uint4 u[PPR / 2];  // (all in flight)
+#pragma unroll
+        for (int i = 0; i < PPR / 2; ++i) {
+            const int g = first + r0 + i * STEP, tok = g / a.G;
+            u[i] = make_uint4(0, 0, 0, 0);
+            if (g < rt.rows)
+                u[i] = *reinterpret_cast<const uint4 *>(
+                    static_cast<const __nv_bfloat16 *>(a.q) + (walk.s.cu0 + tok) * a.q_stride +
+                    (static_cast<long long>(walk.h) * a.G + (g - tok * a.G)) * D + c * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < PPR / 2; ++i)
+            *reinterpret_cast<uint4 *>(q_s + t * C::TILE + (c / 8) * 16384 + sw128_offset(r0 + i * STEP, c % 8)) = u[i];
+        fence_proxy_async_smem();
+        mbar_arrive(q_ready + t);
+    };
+    bool more = walk.next(a, kRows);
+    if (more) load_q();
+    while (more) {
+        const RowTile rt = row_tile(a, walk.s, walk.rt, kRows);
+        const int x0 = walk.x0, x1 = min(walk.x1, rt.count);
         const bool idle = t == 1 && rt.rows - rt.r0 <= 128;  // no rows in this tile
         const int first = rt.r0 + t * 128;                   // first row of the tile
-        // ---- Q rows of this tile into shared memory
-        if (!idle) {
-            constexpr int PPR = D / 8, STEP = 256 / PPR;
-            const int c = row % PPR, r0 = (row + half * 128) / PPR;
-            uint4 u[PPR / 2];  // (all in flight)
-#pragma unroll
-            for (int i = 0; i < PPR / 2; ++i) {
-                const int g = first + r0 + i * STEP, tok = g / a.G;
-                u[i] = make_uint4(0, 0, 0, 0);
-                if (g < rt.rows)
-                    u[i] = *reinterpret_cast<const uint4 *>(
-                        static_cast<const __nv_bfloat16 *>(a.q) + (walk.s.cu0 + tok) * a.q_stride +
-                        (static_cast<long long>(walk.h) * a.G + (g - tok * a.G)) * D + c * 8);
-            }
-#pragma unroll
-            for (int i = 0; i < PPR / 2; ++i)
-                *reinterpret_cast<uint4 *>(q_s + t * C::TILE + (c / 8) * 16384 + sw128_offset(r0 + i * STEP, c % 8)) = u[i];
-            fence_proxy_async_smem();
-            mbar_arrive(q_ready + t);
-        }
         const int mine = first + row, tok = mine / a.G;
         const bool live = mine < rt.rows;
         const int tpos = live ? min(walk.s.off + tok, walk.s.cap - 1) : -1;  // last key that the row sees
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
         const int tmax = walk.s.off + (min(first + 128, rt.rows) - 1) / a.G;
 
         float m = -INFINITY, l = 0.f;
-        for (int x = walk.x0; x < x1; ++x, ++slot) {
+        for (int x = x0; x < x1; ++x, ++slot) {
             if (idle || !ok) continue;
             ok = mbar_wait(meta_full + slot % kMetaSlots, (slot / kMetaSlots) & 1, abort_flag, a.status) &&
                  mbar_wait(bar_s + t, n_s & 1, abort_flag, a.status);
@@ -533,7 +539,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                 const float f = m == -INFINITY ? 1.f : ex2_approx(m - mn);  // (nothing, or NaN, so far)
                 m = mn;
                 l *= f;
-                if (x > walk.x0) {  // O of the tiles before, complete by now or soon
+                if (x > x0) {  // O of the tiles before, complete by now or soon
                     ok = ok && mbar_wait(bar_o + t, (n_s - 1) & 1, abort_flag, a.status);
                     __syncwarp();
                     tc_fence_after();
@@ -600,10 +606,16 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
             mbar_arrive(p_ready + t);
             ++n_s;
         }
+        const bool any = x1 > x0, whole = walk.whole;
+        const long long prow = walk.slot(found) * kRows + t * 128 + row;
+        const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (mine - tok * a.G);
+        // the next segment's Q (the last scores of this one are complete), so that
+        // its first products run beside these outputs
+        more = walk.next(a, kRows);
+        if (more) load_q();
         if (idle) continue;
 
         // ---- outputs: final, or a piece; half of the columns each
-        const bool any = x1 > walk.x0;
         *mine_x = l;
         named_barrier(3 + t, 256);
         l += *other_x;
@@ -612,8 +624,6 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + __log2f(l);
-        const long long prow = walk.slot(found) * kRows + t * 128 + row;
-        const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (mine - tok * a.G);
 #pragma unroll 1
         for (int c = 0; c < D / 2; c += 32) {
             uint32_t o[32];
@@ -624,7 +634,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(any ? __uint_as_float(o[i]) * inv : 0.f);
             const int col = half * (D / 2) + c;
-            if (walk.whole) {
+            if (whole) {
                 uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + col);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -639,7 +649,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
             }
         }
         if (live && half == 0) {
-            if (walk.whole)
+            if (whole)
                 a.lse[orow] = lse2 * kLn2f;
             else
                 a.part_lse[prow] = lse2;
