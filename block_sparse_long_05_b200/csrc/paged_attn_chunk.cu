@@ -84,6 +84,13 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         : "memory");
 }
 
+// 16 bytes to shared memory, zeros if they are not there.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 template <int N>
 __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -433,31 +440,39 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     const float *other_x = halves + (t * 2 + (half ^ 1)) * 128 + row;
     uint32_t slot = 0, n_s = 0;  // key tiles; products awaited
     bool ok = true;
-    // Q rows of the segment's tile into shared memory, if the segment has keys
-    auto load_q = [&]() {
+    // Q rows of the segment's tile to shared memory, if the segment has keys: the
+    // copies are started, and announced later
+    auto start_q = [&]() -> bool {
         const RowTile rt = row_tile(a, walk.s, walk.rt, kRows);
         const int first = rt.r0 + t * 128;
-        if ((t == 1 && rt.rows <= first) || min(walk.x1, rt.count) <= walk.x0) return;
+        if ((t == 1 && rt.rows <= first) || min(walk.x1, rt.count) <= walk.x0) return false;
         constexpr int PPR = D / 8, STEP = 256 / PPR;
         const int c = row % PPR, r0 = (row + half * 128) / PPR;
-        uint4 u[PPR / 2];  // (all in flight)
+        const int step_tok = STEP / a.G, step_g = STEP - step_tok * a.G;
+        int tok = (first + r0) / a.G, g = first + r0 - tok * a.G;
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) + walk.s.cu0 * a.q_stride +
+                                   static_cast<long long>(walk.h) * a.G * D + c * 8;
 #pragma unroll
         for (int i = 0; i < PPR / 2; ++i) {
-            const int g = first + r0 + i * STEP, tok = g / a.G;
-            u[i] = make_uint4(0, 0, 0, 0);
-            if (g < rt.rows)
-                u[i] = *reinterpret_cast<const uint4 *>(
-                    static_cast<const __nv_bfloat16 *>(a.q) + (walk.s.cu0 + tok) * a.q_stride +
-                    (static_cast<long long>(walk.h) * a.G + (g - tok * a.G)) * D + c * 8);
+            const bool there = first + r0 + i * STEP < rt.rows;  // (zeros otherwise)
+            cp_async16(q_s + t * C::TILE + (c / 8) * 16384 + sw128_offset(r0 + i * STEP, c % 8),
+                       there ? src + tok * a.q_stride + g * D : src, there);
+            tok += step_tok;
+            g += step_g;
+            if (g >= a.G) {
+                g -= a.G;
+                ++tok;
+            }
         }
-#pragma unroll
-        for (int i = 0; i < PPR / 2; ++i)
-            *reinterpret_cast<uint4 *>(q_s + t * C::TILE + (c / 8) * 16384 + sw128_offset(r0 + i * STEP, c % 8)) = u[i];
+        return true;
+    };
+    auto announce_q = [&]() {
+        cp_async_wait_all();
         fence_proxy_async_smem();
         mbar_arrive(q_ready + t);
     };
     bool more = walk.next(a, kRows);
-    if (more) load_q();
+    if (more && start_q()) announce_q();
     while (more) {
         const RowTile rt = row_tile(a, walk.s, walk.rt, kRows);
         const int x0 = walk.x0, x1 = min(walk.x1, rt.count);
@@ -471,6 +486,11 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
         // the tile's rows, for the choice of the masked path
         const int tmin = min(walk.s.off + first / a.G, walk.s.cap - 1);
         const int tmax = walk.s.off + (min(first + 128, rt.rows) - 1) / a.G;
+
+        const bool any = x1 > x0, whole = walk.whole;
+        const long long prow = walk.slot(found) * kRows + t * 128 + row;
+        const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (mine - tok * a.G);
+        more = walk.next(a, kRows);  // (here, where the first scores are awaited)
 
         float m = -INFINITY, l = 0.f;
         for (int x = x0; x < x1; ++x, ++slot) {
@@ -509,6 +529,12 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                 if (a.window) bits &= ~below(wpos + 1 - k0) | below(a.sinks - k0);
                 return valid >> (half * 2 + c) & 1 ? bits : 0u;
             };
+            // (at a mask's edge most warps have 32 keys that all rows see)
+            auto mask = [&](uint32_t bits, uint32_t(&y)[32]) {
+                if (!__any_sync(0xFFFFFFFFu, bits != 0xFFFFFFFFu)) return;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = bits >> i & 1 ? y[i] : 0xFF800000u;
+            };
             // ---- the row's maximum
             float g = -INFINITY;
             // (not unrolled: copies of the body run slower, for want of instruction cache)
@@ -516,11 +542,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
             for (int c = 0; c < 2; ++c) {
                 uint32_t y[32];
                 scores(c, y);
-                if (masked) {
-                    const uint32_t bits = visible(c);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) y[i] = bits >> i & 1 ? y[i] : 0xFF800000u;
-                }
+                if (masked) mask(visible(c), y);
                 float g4[4] = {g, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int i = 0; i < 32; i += 8)
@@ -568,11 +590,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                 uint32_t y[32], w[16];
                 scores(c, y);
                 uint32_t bits = 0xFFFFFFFFu;
-                if (masked) {
-                    bits = visible(c);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) y[i] = bits >> i & 1 ? y[i] : 0xFF800000u;
-                }
+                if (masked) mask(bits = visible(c), y);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     float e0, e1;
@@ -606,14 +624,13 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
             mbar_arrive(p_ready + t);
             ++n_s;
         }
-        const bool any = x1 > x0, whole = walk.whole;
-        const long long prow = walk.slot(found) * kRows + t * 128 + row;
-        const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (mine - tok * a.G);
         // the next segment's Q (the last scores of this one are complete), so that
         // its first products run beside these outputs
-        more = walk.next(a, kRows);
-        if (more) load_q();
-        if (idle) continue;
+        const bool fetched = more && start_q();
+        if (idle) {
+            if (fetched) announce_q();
+            continue;
+        }
 
         // ---- outputs: final, or a piece; half of the columns each
         *mine_x = l;
@@ -630,19 +647,32 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
             __syncwarp();
             tmem_ld32(tmem_o + c, o);
             tmem_wait_ld();
-            if (!live) continue;
+            if (fetched && c == 0) announce_q();
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(any ? __uint_as_float(o[i]) * inv : 0.f);
             const int col = half * (D / 2) + c;
             if (whole) {
-                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + col);
+                // two lanes write 32 bytes of a row at a time: first of the even
+                // lane's row, then of the odd one's
+                const bool odd = lane & 1;
+                const long long other = __shfl_xor_sync(0xFFFFFFFFu, live ? orow : -1ll, 1);
+                const long long rows2[2] = {odd ? other : live ? orow : -1ll, odd ? live ? orow : -1ll : other};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    out[i] = make_uint4(bf2(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
-                                        bf2(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
-                                        bf2(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
-                                        bf2(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
-            } else {
+                for (int i = 0; i < 32; i += 16) {
+                    uint32_t w[8], x[4];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) w[k] = bf2(__uint_as_float(o[i + 2 * k]), __uint_as_float(o[i + 2 * k + 1]));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[k] : w[4 + k], 1);
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + col + i + odd * 8;
+                    if (rows2[0] >= 0)
+                        *reinterpret_cast<uint4 *>(out + rows2[0] * D) =
+                            odd ? make_uint4(x[0], x[1], x[2], x[3]) : make_uint4(w[0], w[1], w[2], w[3]);
+                    if (rows2[1] >= 0)
+                        *reinterpret_cast<uint4 *>(out + rows2[1] * D) =
+                            odd ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(x[0], x[1], x[2], x[3]);
+                }
+            } else if (live) {
                 uint4 *out = reinterpret_cast<uint4 *>(a.part_o + prow * D + col);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
