@@ -42,6 +42,19 @@ cudaError_t launch_kv_append(const StepMap &step, const CacheStore &c, const voi
 cudaError_t launch_kv_gather(const StepMap &step, const CacheStore &c, void *k_out, void *v_out,
                              int *status, cudaStream_t st);
 
+// Division of n < 2^31 by a number that the host knows.
+struct Divisor {
+    uint32_t d, mul, shift;
+    explicit Divisor(uint32_t by = 1) : d(by), mul(0), shift(0) {
+        while (shift < 31 && (1u << shift) < by) ++shift;
+        // ceil(2^(31 + shift) / by): exact quotients below 2^31
+        mul = static_cast<uint32_t>(((1ull << (31 + shift)) + by - 1) / by);
+    }
+    __host__ __device__ __forceinline__ uint32_t quotient(uint32_t n) const {
+        return static_cast<uint32_t>((static_cast<uint64_t>(n) * mul) >> 31 >> shift);
+    }
+};
+
 // Attention over pages.
 struct PagedAttn {
     StepMap step;
@@ -52,6 +65,8 @@ struct PagedAttn {
     float *lse = nullptr;    // fp32 [total][Hq]
     int Hq = 0, G = 0;
     int heads = 1;           // kv heads that share a run of key tiles (divides Hkv)
+    int groups = 1;          // Hkv / heads
+    Divisor by_g, by_block;  // G, rows per page
     int row_lo = 0, row_hi = 0x7FFFFFFF;  // rows (tokens * G) of the sequences that a launch takes
     int window = 0, sinks = 0;       // window 0: every key up to the query's position
     const int32_t *ids = nullptr;    // sparse branch: [Bt][K] selected blocks (one row each)

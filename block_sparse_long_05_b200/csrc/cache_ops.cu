@@ -46,19 +46,6 @@ struct Units {
 constexpr float kTiny = 7.888609e-31f;           // 2^-100
 constexpr float kMagic = 12582912.f;             // 1.5 * 2^23
 
-// Division of n < 2^31 by a number that the host knows.
-struct Divisor {
-    uint32_t d, mul, shift;
-    explicit Divisor(uint32_t by) : d(by), mul(0), shift(0) {
-        while (shift < 31 && (1u << shift) < by) ++shift;
-        // ceil(2^(31 + shift) / by): exact quotients below 2^31
-        mul = static_cast<uint32_t>(((1ull << (31 + shift)) + by - 1) / by);
-    }
-    __device__ __forceinline__ uint32_t quotient(uint32_t n) const {
-        return static_cast<uint32_t>((static_cast<uint64_t>(n) * mul) >> 31 >> shift);
-    }
-};
-
 // The step's row offsets in shared memory, unless there are too many: a
 // search for a row's sequence is then a chain of shared-memory reads, not of
 // trips to L2 (which made an append of 24 K rows twice as long).

@@ -178,6 +178,9 @@ msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int nu
     const bool i8 = a.c.k_scales != nullptr;
     for (int h = 1; h <= a.c.Hkv && h <= kSplitMaxHeads; ++h)
         if (a.c.Hkv % h == 0) a.heads = h;
+    a.groups = a.c.Hkv / a.heads;
+    a.by_g = Divisor(a.G);
+    a.by_block = Divisor(a.step.block);
     const int box = split_box_rows(a.step.block);
     CUtensorMap tk, tv;
     if (!store_map(&tk, k_pages, num_pages, a.step.block, a.c.Hkv, a.c.d, box, i8) ||
@@ -206,7 +209,7 @@ msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int nu
     const bool chunk = rows > kSplitMaxRows && !a.ids && tiles * a.c.Hkv * (keys + 2) > 1536;
     // work units are numbered with 31 bits
     const long long row_tiles = chunk ? all / kChunkRows + 2ll * a.step.Bt : 2 * tiles;
-    if (row_tiles * (a.c.Hkv / a.heads) * (keys + 8) >= (1ll << 31)) return MSA_ERR_UNSUPPORTED;
+    if (row_tiles * a.groups * (keys + 8) >= (1ll << 31)) return MSA_ERR_UNSUPPORTED;
     cudaError_t e = cudaSuccess;
     if (chunk) {
         a.row_lo = a.step.Bt > 1 ? kSplitMaxRows + 1 : 0;

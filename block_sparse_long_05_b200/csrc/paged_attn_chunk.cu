@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                         if (I8) {
                             tma_load_3d(dst + i * 32 * D, is_v ? &tm_v : &tm_k, tb, 0, h, z[i]);
                             if (!is_v) {
-                                const int page = z[i] / block;
+                                const int page = static_cast<int>(a.by_block.quotient(z[i]));
                                 const long long so = (static_cast<long long>(page) * a.c.Hkv + h) * block + (z[i] - page * block);
                                 bulk_load(raw_sc + st * 256 + i * 32, a.c.k_scales + so, box * 4, tb);
                                 bulk_load(raw_sc + st * 256 + 128 + i * 32, a.c.v_scales + so, box * 4, tb);
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
                         const int p = pos + i * 32;
                         // (keys before every row's window: their page may be gone)
                         if (p >= hi || (p + box <= lo && p >= a.sinks)) continue;
-                        const int j = p / block;
+                        const int j = a.by_block.quotient(p);
                         const int page = a.step.pm.table[static_cast<long long>(walk.b) * a.step.pm.stride + j];
                         if (page < 0 || page >= a.step.pm.count) {
                             atomicOr(a.status, kDevBadIds);
@@ -448,8 +448,8 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
         if ((t == 1 && rt.rows <= first) || min(walk.x1, rt.count) <= walk.x0) return false;
         constexpr int PPR = D / 8, STEP = 256 / PPR;
         const int c = row % PPR, r0 = (row + half * 128) / PPR;
-        const int step_tok = STEP / a.G, step_g = STEP - step_tok * a.G;
-        int tok = (first + r0) / a.G, g = first + r0 - tok * a.G;
+        const int step_tok = a.by_g.quotient(STEP), step_g = STEP - step_tok * a.G;
+        int tok = a.by_g.quotient(first + r0), g = first + r0 - tok * a.G;
         const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) + walk.s.cu0 * a.q_stride +
                                    static_cast<long long>(walk.h) * a.G * D + c * 8;
 #pragma unroll
@@ -478,14 +478,14 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
         const int x0 = walk.x0, x1 = min(walk.x1, rt.count);
         const bool idle = t == 1 && rt.rows - rt.r0 <= 128;  // no rows in this tile
         const int first = rt.r0 + t * 128;                   // first row of the tile
-        const int mine = first + row, tok = mine / a.G;
+        const int mine = first + row, tok = static_cast<int>(a.by_g.quotient(mine));
         const bool live = mine < rt.rows;
         const int tpos = live ? min(walk.s.off + tok, walk.s.cap - 1) : -1;  // last key that the row sees
         const int wpos = a.window && live ? walk.s.off + tok - a.window : -1;  // a key at or before it is out,
                                                                                // unless a sink
         // the tile's rows, for the choice of the masked path
-        const int tmin = min(walk.s.off + first / a.G, walk.s.cap - 1);
-        const int tmax = walk.s.off + (min(first + 128, rt.rows) - 1) / a.G;
+        const int tmin = min(walk.s.off + static_cast<int>(a.by_g.quotient(first)), walk.s.cap - 1);
+        const int tmax = walk.s.off + static_cast<int>(a.by_g.quotient(min(first + 128, rt.rows) - 1));
 
         const bool any = x1 > x0, whole = walk.whole;
         const long long prow = walk.slot(found) * kRows + t * 128 + row;
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
         if (r0 + r >= rows) break;
-        const int mine = walk.rt * kRows + r0 + r, tok = mine / a.G;
+        const int mine = walk.rt * kRows + r0 + r, tok = static_cast<int>(a.by_g.quotient(mine));
         const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (mine - tok * a.G);
         const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
 #pragma unroll

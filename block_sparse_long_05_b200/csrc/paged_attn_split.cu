@@ -231,7 +231,7 @@ __device__ __noinline__ void merge_pieces(const PagedAttn &a, const RowTile &t, 
                     s += y.y * f;
                     x += pool[(w * ROWS + r) * D + col] * f;
                 }
-                const int row = t.r0 + rg + q + r, tok = row / a.G;
+                const int row = t.r0 + rg + q + r, tok = static_cast<int>(a.by_g.quotient(row));
                 const long long orow = (static_cast<long long>(cu0) + tok) * a.Hq + static_cast<long long>(h) * a.G + (row - tok * a.G);
                 const float inv = s == 0.f ? 0.f : 1.f / s;
                 static_cast<__nv_bfloat16 *>(a.out)[orow * D + col] = __float2bfloat16_rn(x * inv);
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                         }
                         int p;  // key position of the box
                         if (a.ids) {
-                            const int v = x * kKeys + i * 32, slot = v / block;
+                            const int v = x * kKeys + i * 32, slot = a.by_block.quotient(v);
                             const int id = slot < a.K ? a.ids[static_cast<long long>(walk.b) * a.K + slot] : -1;
                             const int N = (a.T + block - 1) / block;
                             if (id < -1 || id >= N) atomicOr(a.status, kDevBadIds);
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                                 p = -1;
                         }
                         if (p < 0) continue;
-                        const int j = p / block;
+                        const int j = a.by_block.quotient(p);
                         const int page = a.step.pm.table[static_cast<long long>(walk.b) * a.step.pm.stride + j];
                         if (page < 0 || page >= a.step.pm.count) {
                             atomicOr(a.status, kDevBadIds);
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                                     tma_load_3d(dv + o, &tm_v, full + st, r * 64, walk.h, zz[i]);
                                 }
                                 if (I8) {
-                                    const int page = zz[i] / block;
+                                    const int page = static_cast<int>(a.by_block.quotient(zz[i]));
                                     const long long so = (static_cast<long long>(page) * a.c.Hkv + walk.h) * block + (zz[i] - page * block);
                                     bulk_load(scales + (2 * st) * kKeys + i * 32, a.c.k_scales + so, box * 4, full + st);
                                     bulk_load(scales + (2 * st + 1) * kKeys + i * 32, a.c.v_scales + so, box * 4, full + st);
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
         for (int rr = 0; rr < R; rr += kCompute / TPR) {
             const int r = rr + tid / TPR, c = tid % TPR;
             if (R % (kCompute / TPR) != 0 && r >= R) continue;  // (whole warps)
-            const int row = t.r0 + r, tok = row / a.G;
+            const int row = t.r0 + r, tok = static_cast<int>(a.by_g.quotient(row));
             uint4 u = make_uint4(0, 0, 0, 0);
             if (row < t.rows)
                 u = *reinterpret_cast<const uint4 *>(
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
             float inv = sum == 0.f ? 0.f : 1.f / sum;
             if (I8 && poison[r]) inv = __uint_as_float(0x7FC00000u);
             const float lse2 = sum == 0.f ? -INFINITY : z + __log2f(sum);
-            const int row = t.r0 + r, tok = row / a.G;
+            const int row = t.r0 + r, tok = static_cast<int>(a.by_g.quotient(row));
             const long long orow = (static_cast<long long>(walk.s.cu0) + tok) * a.Hq + static_cast<long long>(walk.h) * a.G + (row - tok * a.G);
 #pragma unroll
             for (int c = 2 * lane; c < D; c += 64) {

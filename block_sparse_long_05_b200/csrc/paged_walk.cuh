@@ -45,7 +45,7 @@ __device__ __forceinline__ Seq seq_of(const PagedAttn &a, int b, int R) {
         s.off = len - s.n;
         s.nk = (kv + kKeys - 1) / kKeys;
         if (a.window) {
-            const int span = min(s.n, R / a.G + 2);  // tokens of a row tile
+            const int span = min(s.n, static_cast<int>(a.by_g.quotient(R)) + 2);  // tokens of a row tile
             const int near = (a.window + span) / kKeys + 3;
             s.nk = min(s.nk, near + (min(a.sinks, kv) + kKeys - 1) / kKeys);
         }
@@ -61,7 +61,7 @@ __device__ __forceinline__ Seq seq_of(const PagedAttn &a, int b, int R) {
 // what a segment costs beside them (reading Q, writing the output).  (The host
 // keeps the units of a step below 2^31.)
 __device__ __forceinline__ int seq_work(const PagedAttn &a, const Seq &s, int over) {
-    return s.nt * (a.c.Hkv / a.heads) * (s.nk + over);
+    return s.nt * a.groups * (s.nk + over);
 }
 
 // Row tile rt of a sequence: positions of its rows and its key tiles.  Tile
@@ -77,8 +77,8 @@ __device__ __forceinline__ RowTile row_tile(const PagedAttn &a, const Seq &s, in
     RowTile t;
     t.rows = s.n * a.G;
     t.r0 = rt * R;
-    t.tmin = s.off + t.r0 / a.G;
-    t.tmax = s.off + (min(t.r0 + R, t.rows) - 1) / a.G;
+    t.tmin = s.off + static_cast<int>(a.by_g.quotient(t.r0));
+    t.tmax = s.off + static_cast<int>(a.by_g.quotient(min(t.r0 + R, t.rows) - 1));
     t.na = t.skip = 0;
     if (a.ids) {
         t.count = s.nk;
@@ -187,22 +187,26 @@ struct Walk {
     int b, rt, h, x0, x1;
     bool whole;       // all tiles of the segment
     int tile0, end0;  // units of the segment's first tile, and behind its last one
-    int pos, end, off;
+    int pos, end;
+    int y, g, u0;     // the next segment: row tile in the order below, group of heads; its next unit
     int over, hi;     // hi: this CTA's head of those that share the run
     __device__ __forceinline__ Walk(const PagedAttn &a, const Found &f, int over_)
-        : s(f.s), b(f.b), pos(f.start), end(f.run < f.work - f.start ? f.start + f.run : f.work), off(f.off),
-          over(over_), hi(blockIdx.x % a.heads) {}
+        : s(f.s), b(f.b), pos(f.start), end(f.run < f.work - f.start ? f.start + f.run : f.work),
+          over(over_), hi(blockIdx.x % a.heads) {
+        const int units = s.nk + over, seg = f.off / units;
+        u0 = f.off - seg * units;
+        y = seg / a.groups;
+        g = seg - y * a.groups;
+    }
     __device__ __forceinline__ bool next(const PagedAttn &a, int R) {
         while (pos < end) {
-            while (off >= seq_work(a, s, over)) {  // (only after a step; bounded by Bt)
-                off = 0;
+            while (y >= s.nt) {  // (only after a step; bounded by Bt)
+                y = g = 0;
                 if (++b >= a.step.Bt) return false;
                 s = seq_of(a, b, R);
             }
-            const int chunks = a.c.Hkv / a.heads, units = s.nk + over;
-            const int seg = off / units, u0 = off - seg * units;  // segment of the sequence, unit of it
-            const int y = seg / chunks;
-            h = (seg - y * chunks) * a.heads + hi;
+            const int units = s.nk + over, from = u0;
+            h = g * a.heads + hi;
             // last, first, last but one, ...: in a causal chunk late row tiles have more
             // keys than early ones, and a run of several gets its share of both
             rt = y & 1 ? y / 2 : s.nt - 1 - y / 2;
@@ -210,9 +214,13 @@ struct Walk {
             tile0 = pos - u0 + over;
             end0 = pos - u0 + units;
             pos += u1 - u0;
-            off += u1 - u0;
+            u0 = u1 == units ? 0 : u1;
+            if (u1 == units && ++g == a.groups) {
+                g = 0;
+                ++y;
+            }
             if (u1 <= over) continue;
-            x0 = max(u0 - over, 0);
+            x0 = max(from - over, 0);
             x1 = u1 - over;
             whole = x0 == 0 && x1 == s.nk;
             return true;
