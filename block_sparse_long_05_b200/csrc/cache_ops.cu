@@ -19,9 +19,11 @@
 // whose last mantissa bit counts 1, so that no conversion instruction (a quarter
 // of the rate) is needed.  The page of each token is looked up once per token of
 // the CTA's run, into shared memory.  Measured: int8 append of 24573 rows (8
-// heads, d 128) 30 us = 5.0 TB/s, int8 gather of 131072 rows 151 us = 5.4 TB/s;
-// one or four units of codes per thread, or pairs of lanes that read 32 bytes
-// side by side and exchange them in registers, were slower.
+// heads, d 128) 30 us = 5.0 TB/s, int8 gather of 131072 rows 131 us = 6.2 TB/s
+// (151 us where its 32 bytes per thread are stored as two halves, as for
+// outputs that do not begin on 32 bytes; the append's loads gain nothing from
+// it, 31.5 us); one or four units of codes per thread, or pairs of lanes that
+// read 32 bytes side by side and exchange them in registers, were slower.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -209,6 +211,7 @@ struct GatherArgs {
     CacheStore c;
     void *k_out, *v_out;
     Divisor units;  // per token
+    bool wide;      // int8: k_out and v_out on 32 bytes
     int *status;
 };
 
@@ -273,8 +276,14 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const __grid_consta
             o[2 * q] = pack2(f[0], f[1]);
             o[2 * q + 1] = pack2(f[2], f[3]);
         }
-        to[i][0] = make_uint4(o[0], o[1], o[2], o[3]);
-        to[i][1] = make_uint4(o[4], o[5], o[6], o[7]);
+        if (a.wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to[i]), "r"(o[0]),
+                         "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                         : "memory");
+        } else {
+            to[i][0] = make_uint4(o[0], o[1], o[2], o[3]);
+            to[i][1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
     }
 }
 
@@ -321,7 +330,8 @@ cudaError_t launch_kv_append(const StepMap &step, const CacheStore &c, const voi
 
 cudaError_t launch_kv_gather(const StepMap &step, const CacheStore &c, void *k_out, void *v_out,
                              int *status, cudaStream_t st) {
-    const GatherArgs a{step, c, k_out, v_out, Divisor(1), status};
+    const bool wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
+    const GatherArgs a{step, c, k_out, v_out, Divisor(1), wide, status};
     if (c.d == 128) return c.k_scales ? run_gather<8, true>(a, 128, st) : run_gather<16, false>(a, 128, st);
     return c.k_scales ? run_gather<4, true>(a, 64, st) : run_gather<8, false>(a, 64, st);
 }

@@ -212,6 +212,9 @@ msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int nu
     if (row_tiles * a.groups * (keys + 8) >= (1ll << 31)) return MSA_ERR_UNSUPPORTED;
     cudaError_t e = cudaSuccess;
     if (chunk) {
+        // (every SM has a CTA: 144 of 148 with 8 heads in step took 2% longer)
+        while (sms % a.heads || a.c.Hkv % a.heads) --a.heads;
+        a.groups = a.c.Hkv / a.heads;
         a.row_lo = a.step.Bt > 1 ? kSplitMaxRows + 1 : 0;
         e = launch_chunk_attn(a, tk, tv, sms, st);
         a.row_lo = 0;

@@ -108,6 +108,24 @@ def test_append_and_gather(case, i8):
     assert (gk[at:] == 5).all() and (gv[at:] == 5).all(), "rows behind the last sequence"
 
 
+@pytest.mark.parametrize("i8", [False, True])
+def test_gather_into_outputs_that_begin_on_16_bytes(i8):
+    """Outputs that begin on 16 bytes but not on 32 get the same rows."""
+    from block_sparse_long_05_b200 import msa
+    ws = _ws()
+    x = Paged([77, 50], [130, 60], 2, 2, 64, 32, i8=i8)
+    read = msa.kv_gather_i8 if i8 else msa.kv_gather
+    k, v = read(*x.stores(), *x.step(), x.total, ws)
+    for off_k, off_v in ((8, 0), (0, 8), (8, 24)):
+        bufs = [torch.full((x.total * 2 * 64 + 32,), 5.0, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+        outs = [b[o:o + k.numel()].view(k.shape) for b, o in zip(bufs, (off_k, off_v))]
+        read(*x.stores(), *x.step(), x.total, ws, k=outs[0], v=outs[1])
+        assert msa.device_status(ws) == 0
+        assert torch.equal(outs[0], k) and torch.equal(outs[1], v)
+        for b, o in zip(bufs, (off_k, off_v)):
+            assert (b[:o] == 5).all() and (b[o + k.numel():] == 5).all(), "around the output"
+
+
 def test_quantised_rows_that_are_special():
     """Zero rows, rows near the smallest values, single large values, and rows
     with an infinity or a NaN; a row's error is at most half a step."""
