@@ -8,9 +8,12 @@
 //     S = Q K^T (tensor memory), P = 2^(S c - m) in bf16 over S, O += P V
 // with the two row tiles half a step apart, so that one tile's products run
 // while the other tile is in its softmax.  Both products read K and V from
-// shared memory as TMA left them; P never leaves tensor memory.  A softmax
-// thread has a whole row of S in registers: no shuffles.  The running
-// reference m is raised, and O rescaled, only when a score passes it by 2^8.
+// shared memory as TMA left them; P never leaves tensor memory.  Two warpgroups
+// share a row tile, 64 of the 128 keys each: a thread has half a row of S, in
+// two passes of 32 scores (first the maximum, then the weights), and takes no
+// shuffles.  The running reference m may lag behind the maximum, since weights
+// and sums are floating point numbers: it is raised, and O rescaled, only when
+// a score passes it by 2^32, which one vote per tile finds out.
 //
 // int8 pages: eight warps turn the codes into bf16 tiles (exact) ahead of the
 // products; the scales sk multiply the scores and sv the weights in fp32.
@@ -20,7 +23,25 @@
 // rounding is as large, and a second term would double the second product.
 //
 // The work is cut into equal runs of key tiles, one CTA per SM (paged_walk.cuh).
-// Segments in several runs leave fp32 pieces that a second kernel merges.
+// Segments in several runs leave fp32 pieces that a second kernel merges.  At a
+// segment's end the next one's Q is on its way, and its first products run,
+// before this one's outputs are written.
+//
+// Measured: 2048 tokens of 32 heads over 32768 keys, bf16, d 128: 1.18 ms =
+// 0.90 PFLOP/s, 54% of a large library product, 17 us of it the merge; 8192
+// tokens in a window of 1024: 213 us = 0.61 PFLOP/s of visible pairs; six int8
+// contexts of up to 12007 keys with 2215 new tokens of 64 heads: 0.88 ms = 0.62
+// PFLOP/s.  A step of a row tile takes about 4100 clocks: 1700 until the scores
+// of the next 128 keys are there (its own two products and the other tile's,
+// 512 clocks each, and the way there), 500 for the maximum, 150 for the vote,
+// 1450 for the weights.  S and P share columns, and with O they fill tensor
+// memory, so the next scores cannot be computed ahead.  With int8 the scales and
+// the conversion take shared memory's time: 6300 clocks.
+// Slower: weights kept in registers in one pass (1225 against 1184 us; the loop
+// no longer fits the instruction cache), a part of the exponentials as
+// polynomials (+2% with an eighth of them, +7% with a half), two steps of P
+// (bf16 -1%, int8 +6%), a fourth stage for int8 tiles instead of buffers for
+// their codes (+3%).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,7 +59,8 @@ namespace {
 using namespace walk;
 
 constexpr int kRows = kChunkRows;
-constexpr int kOver = 4;       // a segment's start and end cost about as much as four tiles
+constexpr int kOver = 4;       // a segment's start and end cost about as much as two to four
+                               // tiles (2, 3 and 6 here are within 1%)
 constexpr int kMinRun = 5;     // units per run, at least
 constexpr int kMetaSlots = 8;  // tiles whose positions and scales are kept: more than
                                // the rings of K and V tiles hold at a time
@@ -74,14 +96,6 @@ constexpr size_t chunk_smem_bytes() {
     return static_cast<size_t>(2 + C::STAGES) * C::TILE + C::RAWS * (C::RAW + 1024) +
            kMetaSlots * (sizeof(TileMeta) + 8 + (I8 ? 1024 : 0)) + 2048 +
            (2 * C::STAGES + 2 * C::RAWS + 9) * 8 + 64;
-}
-
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_addr(dst)),
-        "l"(src), "r"(bytes), "r"(smem_addr(bar))
-        : "memory");
 }
 
 // 16 bytes to shared memory, zeros if they are not there.
@@ -179,253 +193,253 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
     const int block = a.step.block;
     // (each branch begins with its warpgroup's register request)
     if (warp >= 16) {
-    if (I8 && warp < kProducer) {
-        fewer_registers<C::REST>();
-        // -------------------------------------------------------- int8 -> bf16
-        // Thread: half a row of the tile; rows of 16-byte pieces, swizzled on both
-        // sides so that eight neighbouring rows fall on different banks.
-        const int r = tid & 127, half = warp >> 2 & 1;
-        uint32_t e = 0, slot = 0;
-        bool ok = true;
-        auto convert = [&](bool is_v) {
-            const uint32_t rs = e % RS, st = e % C::STAGES;
-            ok = mbar_wait(raw_full + rs, (e / RS) & 1, abort_flag, a.status);
-            if (ok && e >= static_cast<uint32_t>(C::STAGES))
-                ok = mbar_wait(empty + st, ((e / C::STAGES) & 1) ^ 1, abort_flag, a.status);
-            if (!ok) return;
-            const unsigned char *src = raw + rs * C::RAW;
-            unsigned char *dst = ring + st * C::TILE;
-            if (!is_v && half == 0) {
-                float *sc = scales + slot % kMetaSlots * 256;
-                sc[r] = raw_sc[rs * 256 + r];
-                sc[128 + r] = raw_sc[rs * 256 + 128 + r];
-                mbar_arrive(meta_full + slot % kMetaSlots);
-                ++slot;
-            }
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const int p = half * (D / 32) + i;
-                const uint32_t at = D == 128 ? sw128_offset(r, p) : r * 64u + ((p ^ ((r >> 1) & 3u)) << 4);
-                const uint4 u = *reinterpret_cast<const uint4 *>(src + at);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                uint32_t o[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    o[2 * k] = s8x2_bf16(__byte_perm(w[k], 0, 0x1100));
-                    o[2 * k + 1] = s8x2_bf16(__byte_perm(w[k], 0, 0x3322));
+        if (I8 && warp < kProducer) {
+            fewer_registers<C::REST>();
+            // -------------------------------------------------------- int8 -> bf16
+            // Thread: half a row of the tile; rows of 16-byte pieces, swizzled on both
+            // sides so that eight neighbouring rows fall on different banks.
+            const int r = tid & 127, half = warp >> 2 & 1;
+            uint32_t e = 0, slot = 0;
+            bool ok = true;
+            auto convert = [&](bool is_v) {
+                const uint32_t rs = e % RS, st = e % C::STAGES;
+                ok = mbar_wait(raw_full + rs, (e / RS) & 1, abort_flag, a.status);
+                if (ok && e >= static_cast<uint32_t>(C::STAGES))
+                    ok = mbar_wait(empty + st, ((e / C::STAGES) & 1) ^ 1, abort_flag, a.status);
+                if (!ok) return;
+                const unsigned char *src = raw + rs * C::RAW;
+                unsigned char *dst = ring + st * C::TILE;
+                if (!is_v && half == 0) {
+                    float *sc = scales + slot % kMetaSlots * 256;
+                    sc[r] = raw_sc[rs * 256 + r];
+                    sc[128 + r] = raw_sc[rs * 256 + 128 + r];
+                    mbar_arrive(meta_full + slot % kMetaSlots);
+                    ++slot;
                 }
-                unsigned char *to = dst + p / 4 * 16384;
-                *reinterpret_cast<uint4 *>(to + sw128_offset(r, p % 4 * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4 *>(to + sw128_offset(r, p % 4 * 2 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(full + st);
-            mbar_arrive(raw_empty + rs);
-            ++e;
-        };
-        while (ok && walk.next(a, kRows)) {
-            const RowTile t = row_tile(a, walk.s, walk.rt, kRows);
-            const int n = min(walk.x1, t.count) - walk.x0;
-            for (int x = 0; x < n && ok; ++x) {
-                convert(false);
-                if (x > 0 && ok) convert(true);
-            }
-            if (n > 0 && ok) convert(true);
-        }
-        return;
-    }
-    fewer_registers<C::REST>();
-    if (warp == kProducer) {
-        // -------------------------------------------------------- producer
-        // Order of the tiles: K 0, then K x + 1 and V x in turn.
-        uint32_t e = 0, edges = 0;  // tiles issued; V tiles with zeros
-        uint32_t slot = 0;          // key tiles announced
-        const int box = min(block, kKeys);
-        bool ok = true;
-        // One tile of K or V: keys at pos.. (valid quarters), store rows z.  Some
-        // row of the segment sees the keys below hi that are sinks or from lo on.
-        auto load = [&](bool is_v, int pos, int valid, const int (&z)[4], int h, int lo, int hi, uint32_t sl) {
-            const uint32_t st = e % (I8 ? RS : C::STAGES), ph = e / (I8 ? RS : C::STAGES);
-            uint64_t *fb = I8 ? raw_full + st : full + st;
-            unsigned char *dst = I8 ? raw + st * C::RAW : ring + st * C::TILE;
-            // rows of V that no row may use are zeroed (bf16: they may hold anything,
-            // and 0 times it need not be 0)
-            const bool zeros = !I8 && is_v && (valid != 15 || pos + kKeys > hi || (pos < lo && pos + kKeys > a.sinks));
-            if (lane == 0) {
-                if (e >= static_cast<uint32_t>(I8 ? RS : C::STAGES))
-                    ok = mbar_wait((I8 ? raw_empty : empty) + st, (ph & 1) ^ 1, abort_flag, a.status);
-                if (ok) {
-                    if (!is_v) {
-                        meta[sl % kMetaSlots].pos = pos;
-                        meta[sl % kMetaSlots].valid = valid;
-                        if (!I8) mbar_arrive(meta_full + sl % kMetaSlots);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const int p = half * (D / 32) + i;
+                    const uint32_t at = D == 128 ? sw128_offset(r, p) : r * 64u + ((p ^ ((r >> 1) & 3u)) << 4);
+                    const uint4 u = *reinterpret_cast<const uint4 *>(src + at);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        o[2 * k] = s8x2_bf16(__byte_perm(w[k], 0, 0x1100));
+                        o[2 * k + 1] = s8x2_bf16(__byte_perm(w[k], 0, 0x3322));
                     }
-                    uint64_t *tb = zeros ? edge : fb;
-                    int boxes = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) boxes += i * 32 % box == 0 && (valid >> i & 1);
-                    if (boxes == 0)
-                        mbar_arrive(tb);
-                    else
-                        mbar_arrive_expect_tx(tb, boxes * box * (D * EB + (I8 && !is_v ? 8 : 0)));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (i * 32 % box != 0 || !(valid >> i & 1)) continue;
-                        if (I8) {
-                            tma_load_3d(dst + i * 32 * D, is_v ? &tm_v : &tm_k, tb, 0, h, z[i]);
-                            if (!is_v) {
-                                const int page = static_cast<int>(a.by_block.quotient(z[i]));
-                                const long long so = (static_cast<long long>(page) * a.c.Hkv + h) * block + (z[i] - page * block);
-                                bulk_load(raw_sc + st * 256 + i * 32, a.c.k_scales + so, box * 4, tb);
-                                bulk_load(raw_sc + st * 256 + 128 + i * 32, a.c.v_scales + so, box * 4, tb);
-                            }
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < C::REGS; ++r)
-                                tma_load_3d(dst + r * 16384 + i * 4096, is_v ? &tm_v : &tm_k, tb, r * 64, h, z[i]);
-                        }
-                    }
-                    if (zeros) ok = mbar_wait(edge, edges & 1, abort_flag, a.status);
-                }
-            }
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-            if (ok && zeros) {
-                ++edges;
-                mbar_try_wait(edge, (edges - 1) & 1);  // (complete: orders this lane's writes behind the copy's)
-                for (int r = lane; r < kKeys; r += 32) {
-                    const int p = pos + r;
-                    if ((valid >> (r / 32) & 1) && p < hi && (p >= lo || p < a.sinks)) continue;
-#pragma unroll
-                    for (int c = 0; c < 8 * C::REGS; ++c)
-                        *reinterpret_cast<uint4 *>(dst + c / 8 * 16384 + r * 128 + ((c + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    unsigned char *to = dst + p / 4 * 16384;
+                    *reinterpret_cast<uint4 *>(to + sw128_offset(r, p % 4 * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(to + sw128_offset(r, p % 4 * 2 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
                 fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(fb);
-            }
-            if (ok) ++e;
-        };
-        while (ok && walk.next(a, kRows)) {
-            const RowTile t = row_tile(a, walk.s, walk.rt, kRows);
-            const int x1 = min(walk.x1, t.count);
-            const int hi = min(t.tmax + 1, walk.s.cap);
-            const int lo = a.window ? t.tmin - a.window + 1 : 0;
-            int vp = 0, vv = 0, vz[4] = {0, 0, 0, 0};  // the V tile that follows the next K tile
-            for (int xb = walk.x0; xb < x1 && ok; xb += 32) {
-                int pos = 0, valid = 0, z[4] = {0, 0, 0, 0};
-                const int x = xb + lane;
-                if (x < x1) {
-                    pos = (x < t.na ? x : x + t.skip) * kKeys;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (i > 0 && i * 32 % box != 0) {
-                            valid |= (valid >> (i - 1) & 1) << i;
-                            continue;
-                        }
-                        const int p = pos + i * 32;
-                        // (keys before every row's window: their page may be gone)
-                        if (p >= hi || (p + box <= lo && p >= a.sinks)) continue;
-                        const int j = a.by_block.quotient(p);
-                        const int page = a.step.pm.table[static_cast<long long>(walk.b) * a.step.pm.stride + j];
-                        if (page < 0 || page >= a.step.pm.count) {
-                            atomicOr(a.status, kDevBadIds);
-                            continue;
-                        }
-                        valid |= 1 << i;
-                        z[i] = page * block + (p - j * block);
-                    }
-                }
-                const int m = min(32, x1 - xb);
-                for (int y = 0; y < m && ok; ++y) {
-                    const int p = __shfl_sync(0xFFFFFFFFu, pos, y), v = __shfl_sync(0xFFFFFFFFu, valid, y);
-                    int zz[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) zz[i] = __shfl_sync(0xFFFFFFFFu, z[i], y);
-                    load(false, p, v, zz, walk.h, lo, hi, slot);
-                    ++slot;
-                    if (xb + y > walk.x0 && ok) load(true, vp, vv, vz, walk.h, lo, hi, 0);
-                    vp = p;
-                    vv = v;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) vz[i] = zz[i];
-                }
-            }
-            if (ok && x1 > walk.x0) load(true, vp, vv, vz, walk.h, lo, hi, 0);
-        }
-        // after an abort: the copies have landed before the CTA ends
-        if (!ok && lane == 0) {
-            const uint32_t n = I8 ? RS : C::STAGES;
-            for (uint32_t i = e > n ? e - n : 0; i < e; ++i) {
-                const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait((I8 ? raw_full : full) + i % n, (i / n) & 1))
-                    if (global_timer_ns() - t0 > kWaitLimitNs / 4) break;
-            }
-        }
-        return;
-    }
-
-    if (warp == kProducts) {
-        // -------------------------------------------------------- products
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false), idesc_o = idesc_bf16_f32(128, D, true);
-            const uint64_t q0 = sdesc_sw128(smem_addr(q_s), 16, 1024), k0 = sdesc_sw128(smem_addr(ring), 16, 1024);
-            const uint64_t v0 = sdesc_sw128(smem_addr(ring), 16384, 1024);
-            uint32_t e = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // ring tiles taken; Q and weights awaited
-            bool ok = true;
-            auto scores = [&](int t, uint32_t st) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t o = (k / 4) * 16384 + (k % 4) * 32;
-                    umma_bf16(tmem + t * 128, q0 + ((t * C::TILE + o) >> 4), k0 + ((st * C::TILE + o) >> 4), idesc_s, k > 0);
-                }
-                umma_commit(bar_s + t);
+                mbar_arrive(full + st);
+                mbar_arrive(raw_empty + rs);
+                ++e;
             };
             while (ok && walk.next(a, kRows)) {
-                const RowTile rt = row_tile(a, walk.s, walk.rt, kRows);
-                const int n = min(walk.x1, rt.count) - walk.x0;
-                const int tiles = rt.rows - rt.r0 > 128 ? 2 : 1;
-                if (n <= 0) continue;
-                for (int t = 0; t < tiles && ok; ++t) ok = mbar_wait(q_ready + t, nq[t]++ & 1, abort_flag, a.status);
-                if (!ok) break;
-                uint32_t st = e % C::STAGES;
-                if (!(ok = mbar_wait(full + st, (e / C::STAGES) & 1, abort_flag, a.status))) break;
-                tc_fence_after();
-                for (int t = 0; t < tiles; ++t) scores(t, st);
-                umma_commit(empty + st);
-                ++e;
+                const RowTile t = row_tile(a, walk.s, walk.rt, kRows);
+                const int n = min(walk.x1, t.count) - walk.x0;
                 for (int x = 0; x < n && ok; ++x) {
-                    const bool more = x + 1 < n;
-                    const uint32_t ek = e, ev = more ? e + 1 : e;
-                    const uint32_t sk = ek % C::STAGES, sv = ev % C::STAGES;
-                    if (!(ok = mbar_wait(full + sv, (ev / C::STAGES) & 1, abort_flag, a.status))) break;
-                    for (int t = 0; t < tiles; ++t) {
-                        if (!(ok = mbar_wait(p_ready + t, np[t]++ & 1, abort_flag, a.status))) break;
-                        tc_fence_after();
+                    convert(false);
+                    if (x > 0 && ok) convert(true);
+                }
+                if (n > 0 && ok) convert(true);
+            }
+            return;
+        }
+        fewer_registers<C::REST>();
+        if (warp == kProducer) {
+            // -------------------------------------------------------- producer
+            // Order of the tiles: K 0, then K x + 1 and V x in turn.
+            uint32_t e = 0, edges = 0;  // tiles issued; V tiles with zeros
+            uint32_t slot = 0;          // key tiles announced
+            const int box = min(block, kKeys);
+            bool ok = true;
+            // One tile of K or V: keys at pos.. (valid quarters), store rows z.  Some
+            // row of the segment sees the keys below hi that are sinks or from lo on.
+            auto load = [&](bool is_v, int pos, int valid, const int (&z)[4], int h, int lo, int hi, uint32_t sl) {
+                const uint32_t st = e % (I8 ? RS : C::STAGES), ph = e / (I8 ? RS : C::STAGES);
+                uint64_t *fb = I8 ? raw_full + st : full + st;
+                unsigned char *dst = I8 ? raw + st * C::RAW : ring + st * C::TILE;
+                // rows of V that no row may use are zeroed (bf16: they may hold anything,
+                // and 0 times it need not be 0)
+                const bool zeros = !I8 && is_v && (valid != 15 || pos + kKeys > hi || (pos < lo && pos + kKeys > a.sinks));
+                if (lane == 0) {
+                    if (e >= static_cast<uint32_t>(I8 ? RS : C::STAGES))
+                        ok = mbar_wait((I8 ? raw_empty : empty) + st, (ph & 1) ^ 1, abort_flag, a.status);
+                    if (ok) {
+                        if (!is_v) {
+                            meta[sl % kMetaSlots].pos = pos;
+                            meta[sl % kMetaSlots].valid = valid;
+                            if (!I8) mbar_arrive(meta_full + sl % kMetaSlots);
+                        }
+                        uint64_t *tb = zeros ? edge : fb;
+                        int boxes = 0;
 #pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)
-                            umma_bf16_tmem_a(tmem + 256 + t * 128, tmem + t * 128 + (k / 4) * 64 + (k % 4) * 8,
-                                             v0 + ((sv * C::TILE + k * 16 * 128) >> 4), idesc_o, x > 0 || k > 0);
-                        umma_commit(bar_o + t);
-                        if (more) {
-                            if (t == 0 && !(ok = mbar_wait(full + sk, (ek / C::STAGES) & 1, abort_flag, a.status))) break;
-                            tc_fence_after();
-                            scores(t, sk);
+                        for (int i = 0; i < 4; ++i) boxes += i * 32 % box == 0 && (valid >> i & 1);
+                        if (boxes == 0)
+                            mbar_arrive(tb);
+                        else
+                            mbar_arrive_expect_tx(tb, boxes * box * (D * EB + (I8 && !is_v ? 8 : 0)));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (i * 32 % box != 0 || !(valid >> i & 1)) continue;
+                            if (I8) {
+                                tma_load_3d(dst + i * 32 * D, is_v ? &tm_v : &tm_k, tb, 0, h, z[i]);
+                                if (!is_v) {
+                                    const int page = static_cast<int>(a.by_block.quotient(z[i]));
+                                    const long long so = (static_cast<long long>(page) * a.c.Hkv + h) * block + (z[i] - page * block);
+                                    bulk_load(raw_sc + st * 256 + i * 32, a.c.k_scales + so, box * 4, tb);
+                                    bulk_load(raw_sc + st * 256 + 128 + i * 32, a.c.v_scales + so, box * 4, tb);
+                                }
+                            } else {
+#pragma unroll
+                                for (int r = 0; r < C::REGS; ++r)
+                                    tma_load_3d(dst + r * 16384 + i * 4096, is_v ? &tm_v : &tm_k, tb, r * 64, h, z[i]);
+                            }
+                        }
+                        if (zeros) ok = mbar_wait(edge, edges & 1, abort_flag, a.status);
+                    }
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                if (ok && zeros) {
+                    ++edges;
+                    mbar_try_wait(edge, (edges - 1) & 1);  // (complete: orders this lane's writes behind the copy's)
+                    for (int r = lane; r < kKeys; r += 32) {
+                        const int p = pos + r;
+                        if ((valid >> (r / 32) & 1) && p < hi && (p >= lo || p < a.sinks)) continue;
+#pragma unroll
+                        for (int c = 0; c < 8 * C::REGS; ++c)
+                            *reinterpret_cast<uint4 *>(dst + c / 8 * 16384 + r * 128 + ((c + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(fb);
+                }
+                if (ok) ++e;
+            };
+            while (ok && walk.next(a, kRows)) {
+                const RowTile t = row_tile(a, walk.s, walk.rt, kRows);
+                const int x1 = min(walk.x1, t.count);
+                const int hi = min(t.tmax + 1, walk.s.cap);
+                const int lo = a.window ? t.tmin - a.window + 1 : 0;
+                int vp = 0, vv = 0, vz[4] = {0, 0, 0, 0};  // the V tile that follows the next K tile
+                for (int xb = walk.x0; xb < x1 && ok; xb += 32) {
+                    int pos = 0, valid = 0, z[4] = {0, 0, 0, 0};
+                    const int x = xb + lane;
+                    if (x < x1) {
+                        pos = (x < t.na ? x : x + t.skip) * kKeys;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (i > 0 && i * 32 % box != 0) {
+                                valid |= (valid >> (i - 1) & 1) << i;
+                                continue;
+                            }
+                            const int p = pos + i * 32;
+                            // (keys before every row's window: their page may be gone)
+                            if (p >= hi || (p + box <= lo && p >= a.sinks)) continue;
+                            const int j = a.by_block.quotient(p);
+                            const int page = a.step.pm.table[static_cast<long long>(walk.b) * a.step.pm.stride + j];
+                            if (page < 0 || page >= a.step.pm.count) {
+                                atomicOr(a.status, kDevBadIds);
+                                continue;
+                            }
+                            valid |= 1 << i;
+                            z[i] = page * block + (p - j * block);
                         }
                     }
-                    if (!ok) break;
-                    umma_commit(empty + sv);
-                    if (more) umma_commit(empty + sk);
-                    e = ev + 1;
+                    const int m = min(32, x1 - xb);
+                    for (int y = 0; y < m && ok; ++y) {
+                        const int p = __shfl_sync(0xFFFFFFFFu, pos, y), v = __shfl_sync(0xFFFFFFFFu, valid, y);
+                        int zz[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) zz[i] = __shfl_sync(0xFFFFFFFFu, z[i], y);
+                        load(false, p, v, zz, walk.h, lo, hi, slot);
+                        ++slot;
+                        if (xb + y > walk.x0 && ok) load(true, vp, vv, vz, walk.h, lo, hi, 0);
+                        vp = p;
+                        vv = v;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) vz[i] = zz[i];
+                    }
+                }
+                if (ok && x1 > walk.x0) load(true, vp, vv, vz, walk.h, lo, hi, 0);
+            }
+            // after an abort: the copies have landed before the CTA ends
+            if (!ok && lane == 0) {
+                const uint32_t n = I8 ? RS : C::STAGES;
+                for (uint32_t i = e > n ? e - n : 0; i < e; ++i) {
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait((I8 ? raw_full : full) + i % n, (i / n) & 1))
+                        if (global_timer_ns() - t0 > kWaitLimitNs / 4) break;
                 }
             }
+            return;
         }
-        __syncwarp();
-        named_barrier(2, 512 + 32);  // the softmax warps have read their last outputs
-        tmem_dealloc(tmem, 512);
-        return;
-    }
 
-    return;
+        if (warp == kProducts) {
+            // -------------------------------------------------------- products
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false), idesc_o = idesc_bf16_f32(128, D, true);
+                const uint64_t q0 = sdesc_sw128(smem_addr(q_s), 16, 1024), k0 = sdesc_sw128(smem_addr(ring), 16, 1024);
+                const uint64_t v0 = sdesc_sw128(smem_addr(ring), 16384, 1024);
+                uint32_t e = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // ring tiles taken; Q and weights awaited
+                bool ok = true;
+                auto scores = [&](int t, uint32_t st) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t o = (k / 4) * 16384 + (k % 4) * 32;
+                        umma_bf16(tmem + t * 128, q0 + ((t * C::TILE + o) >> 4), k0 + ((st * C::TILE + o) >> 4), idesc_s, k > 0);
+                    }
+                    umma_commit(bar_s + t);
+                };
+                while (ok && walk.next(a, kRows)) {
+                    const RowTile rt = row_tile(a, walk.s, walk.rt, kRows);
+                    const int n = min(walk.x1, rt.count) - walk.x0;
+                    const int tiles = rt.rows - rt.r0 > 128 ? 2 : 1;
+                    if (n <= 0) continue;
+                    for (int t = 0; t < tiles && ok; ++t) ok = mbar_wait(q_ready + t, nq[t]++ & 1, abort_flag, a.status);
+                    if (!ok) break;
+                    uint32_t st = e % C::STAGES;
+                    if (!(ok = mbar_wait(full + st, (e / C::STAGES) & 1, abort_flag, a.status))) break;
+                    tc_fence_after();
+                    for (int t = 0; t < tiles; ++t) scores(t, st);
+                    umma_commit(empty + st);
+                    ++e;
+                    for (int x = 0; x < n && ok; ++x) {
+                        const bool more = x + 1 < n;
+                        const uint32_t ek = e, ev = more ? e + 1 : e;
+                        const uint32_t sk = ek % C::STAGES, sv = ev % C::STAGES;
+                        if (!(ok = mbar_wait(full + sv, (ev / C::STAGES) & 1, abort_flag, a.status))) break;
+                        for (int t = 0; t < tiles; ++t) {
+                            if (!(ok = mbar_wait(p_ready + t, np[t]++ & 1, abort_flag, a.status))) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                umma_bf16_tmem_a(tmem + 256 + t * 128, tmem + t * 128 + (k / 4) * 64 + (k % 4) * 8,
+                                                 v0 + ((sv * C::TILE + k * 16 * 128) >> 4), idesc_o, x > 0 || k > 0);
+                            umma_commit(bar_o + t);
+                            if (more) {
+                                if (t == 0 && !(ok = mbar_wait(full + sk, (ek / C::STAGES) & 1, abort_flag, a.status))) break;
+                                tc_fence_after();
+                                scores(t, sk);
+                            }
+                        }
+                        if (!ok) break;
+                        umma_commit(empty + sv);
+                        if (more) umma_commit(empty + sk);
+                        e = ev + 1;
+                    }
+                }
+            }
+            __syncwarp();
+            named_barrier(2, 512 + 32);  // the softmax warps have read their last outputs
+            tmem_dealloc(tmem, 512);
+            return;
+        }
+
+        return;
     }
 
     more_registers<C::SOFTMAX>();

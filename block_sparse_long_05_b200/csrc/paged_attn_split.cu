@@ -25,7 +25,7 @@
 // draws most of the weight) may make up the output: with 20 bits their
 // rounding would show.  sk, sv and the digits' weights are applied in fp32.  (A kernel that turned
 // the codes into bf16 fragments for mma.sync spent 700 instructions per warp
-// on 16 keys and reached 2.6 TB/s; this one spends about 300 on 32.)
+// on 16 keys and reached 2.6 TB/s.)
 // bf16 pages take Q as it is and P as two bf16 terms (hi + lo, 16 bits).
 //
 //  - The key tiles of all (sequence, row tile, kv head) segments form one
@@ -99,14 +99,6 @@ constexpr size_t split_smem_bytes() {
     using T = Tile<D, I8, R>;
     return 1024 + static_cast<size_t>(T::STAGES) * T::STAGE + round_up(T::QBYTES, 1024) +
            2 * round_up(T::PBYTES, 1024) + (I8 ? T::STAGES * kScaleBytes : 0) + 2 * (R + 4) * 16 + R * 36 + 16 + T::STAGES * (sizeof(StageMeta) + 16) + 72;
-}
-
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_addr(dst)),
-        "l"(src), "r"(bytes), "r"(smem_addr(bar))
-        : "memory");
 }
 
 // Maximum over the warp (a NaN counts as absent).
@@ -443,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
             while (ok && walk.next(a, R)) {
                 const RowTile t = row_tile(a, walk.s, walk.rt, R);
                 const int x1 = min(walk.x1, t.count);
+                if (x1 <= walk.x0) continue;  // nothing to see: Q is not announced
                 ok = mbar_wait(q_ready, segs++ & 1, abort_flag, a.status);
                 for (int x = walk.x0; x < x1 && ok; ++x, ++it) {
                     const uint32_t st = it % T::STAGES, tmem_s = tmem + (it & 1) * (T::NS + T::NO);
@@ -460,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                     umma_commit(bar_s + (it & 1));
                     if (x > walk.x0) outputs(it - 1);
                 }
-                if (ok && x1 > walk.x0) outputs(it - 1);
+                if (ok) outputs(it - 1);
             }
         }
         __syncwarp();
@@ -538,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
             }
         }
         fence_proxy_async_smem();
-        mbar_arrive(q_ready);
+        if (x1 > walk.x0) mbar_arrive(q_ready);
         named_barrier(1, kCompute);  // rowpos, qscale, maxima
 
         float o[R], l[R];  // this column's sums, this key lane's weights

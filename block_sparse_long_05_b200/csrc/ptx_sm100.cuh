@@ -120,6 +120,16 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// Bulk (non-tensor) copy global -> shared.  Both addresses 16-byte aligned, size
+// a multiple of 16.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            smem_addr(dst)),
+        "l"(src), "r"(bytes), "r"(smem_addr(bar))
+        : "memory");
+}
+
 // Bulk (non-tensor) copy shared -> global with an L2 eviction policy,
 // tracked by bulk groups.  Both addresses 16-byte aligned, size a multiple
 // of 16.

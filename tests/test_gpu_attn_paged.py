@@ -111,6 +111,15 @@ def test_no_rows():
 
 
 @pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("n, count", [(1, 900), (9, 300), (260, 24)])
+def test_many_rows_without_keys(n, count, i8):
+    """Long runs of row tiles that see nothing, with contexts between them."""
+    ts = [0 if b % 7 else n + 130 for b in range(count)]
+    ts[-1] = 0
+    _both(Paged([n] * count, ts, 4, 2, 64, 64, i8=i8))
+
+
+@pytest.mark.parametrize("i8", [False, True])
 @pytest.mark.parametrize("n", [1, 150])
 def test_missing_pages(n, i8):
     """Keys of a page that does not exist are left out and reported."""
