@@ -176,9 +176,14 @@ msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int nu
     const int sms = num_sms_current();
     if (sms <= 0) return MSA_ERR_CUDA;
     const bool i8 = a.c.k_scales != nullptr;
-    for (int h = 1; h <= a.c.Hkv && h <= kSplitMaxHeads; ++h)
-        if (a.c.Hkv % h == 0) a.heads = h;
-    a.groups = a.c.Hkv / a.heads;
+    // kv heads whose CTAs share a run: as many as may be; `all`: so that no CTA of
+    // that many is left over (chunks: with 8 heads in step on 144 of 148 SMs they
+    // took 2% longer)
+    auto share = [&](int all) {
+        for (int h = 1; h <= a.c.Hkv && h <= kSplitMaxHeads; ++h)
+            if (a.c.Hkv % h == 0 && all % h == 0) a.heads = h;
+        a.groups = a.c.Hkv / a.heads;
+    };
     a.by_g = Divisor(a.G);
     a.by_block = Divisor(a.step.block);
     const int box = split_box_rows(a.step.block);
@@ -207,18 +212,17 @@ msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int nu
     // 53 / 25; 64 over 4000: 45 / 38.  In a batch the split kernel then takes the
     // sequences with few rows; a hint that is too low costs time, not rows.
     const bool chunk = rows > kSplitMaxRows && !a.ids && tiles * a.c.Hkv * (keys + 2) > 1536;
+    share(chunk ? sms : 0);
     // work units are numbered with 31 bits
     const long long row_tiles = chunk ? all / kChunkRows + 2ll * a.step.Bt : 2 * tiles;
     if (row_tiles * a.groups * (keys + 8) >= (1ll << 31)) return MSA_ERR_UNSUPPORTED;
     cudaError_t e = cudaSuccess;
     if (chunk) {
-        // (every SM has a CTA: 144 of 148 with 8 heads in step took 2% longer)
-        while (sms % a.heads || a.c.Hkv % a.heads) --a.heads;
-        a.groups = a.c.Hkv / a.heads;
         a.row_lo = a.step.Bt > 1 ? kSplitMaxRows + 1 : 0;
         e = launch_chunk_attn(a, tk, tv, sms, st);
         a.row_lo = 0;
         a.row_hi = kSplitMaxRows;
+        share(0);
     }
     if (e == cudaSuccess && (!chunk || a.step.Bt > 1))
         e = launch_split_attn(a, rows, tk, tv, sms, st);

@@ -206,8 +206,8 @@ MSA_API msa_status msa_sparse_attn_paged(const void *q, const void *k_pages, con
  * their whole context, and attention in a window with first tokens that stay
  * visible.  A step of a batch is described by two device arrays:
  *   cu      [Bt + 1] int32: packed rows cu[b] .. cu[b+1]-1 belong to sequence
- *           b (cu[0] = 0, ascending); rows at or behind cu[Bt] are neither
- *           read nor written, so a padded buffer needs no copy;
+ *           b (cu[0] = 0, ascending); rows at or behind cu[Bt] do not matter
+ *           and are not written, so a padded buffer needs no copy;
  *   kv_len  [Bt] int32: length of each context, this step's tokens included.
  * Row i of the n_b = cu[b+1] - cu[b] rows of sequence b stands at position
  * t = kv_len[b] - n_b + i.  The arrays are read when the kernels run: a
@@ -220,7 +220,8 @@ MSA_API msa_status msa_sparse_attn_paged(const void *q, const void *k_pages, con
  * it is written, a row x of d values gets (all in fp32)
  *     amax = max |x_i|, inv = 127 / amax, code_i = rint(x_i * inv), scale = amax / 127.
  * Rows with amax < 2^-100 are stored as zeros; a row that holds an infinity
- * or a NaN gets scale NaN, so that it reads back as NaN.
+ * or a NaN gets scale NaN, so that it reads back as NaN.  Scales that a
+ * caller brings from elsewhere are not negative.
  *
  * Pages are found as in the paged decode calls above: logical block j of
  * sequence b is page_table[b*page_stride + j].  A page id outside
@@ -228,8 +229,9 @@ MSA_API msa_status msa_sparse_attn_paged(const void *q, const void *k_pages, con
  * and reported as MSA_ERR_BAD_IDS in the status word (msa_device_status).
  * Limits (MSA_ERR_UNSUPPORTED): d, d_idx in {64, 128}; block 32, 64 or a
  * multiple of 128; num_pages*block < 2^31; page_stride*block, total < 2^30;
- * total*Hkv*d < 2^33 (append, gather); total*Hq < 2^31.  Any Hq that Hkv
- * divides.  Row strides (elements) are multiples of 8 and at least a row
+ * total*Hkv*d < 2^33 (append, gather); total*Hq < 2^31; attention: fewer than
+ * 2^31 (row tile, kv head, 128 keys) triples, counted with the page table's
+ * whole width (or the window).  Any Hq that Hkv divides.  Row strides (elements) are multiples of 8 and at least a row
  * long: k, v and q may be parts of one projection's output.  All base
  * pointers are 16-byte aligned but for int32 arrays and lse (4).  total = 0
  * is a step without rows: MSA_OK, nothing enqueued.
@@ -293,7 +295,9 @@ MSA_API msa_status msa_kv_gather_i8(const int8_t *k_pages, const int8_t *v_pages
  * values every q_stride elements.  A query at position t sees the keys
  *     j <= t  with  window == 0  or  j > t - window  or  j < sinks
  * (window > 0: the last `window` keys, itself among them, and the first
- * `sinks` ones; sinks is ignored without a window).  Scale 1/sqrt(d).
+ * `sinks` ones; sinks is ignored without a window).  Scale 1/sqrt(d).  Pages
+ * that lie wholly before every window and behind the sinks are not looked up:
+ * their table entries may be stale.
  * out [total][Hq][d] bf16 (fp32 sums, rounded once), lse [total][Hq] fp32
  * (natural log); a row that sees no key gets out 0 and lse -inf.
  * max_q: the largest n_b of the step, or 0 if the caller does not know it; it
@@ -321,7 +325,8 @@ MSA_API msa_status msa_attn_paged_i8(const void *q, int64_t q_stride, const int8
 /*
  * The sparse branch of a decode step on int8 pages: msa_sparse_attn_paged
  * (same ids, same keys) with the 8-bit stores and the output types of this
- * section: out [Bt][1][Hq][d] bf16, lse [Bt][1][Hq] fp32.  K <= 32.
+ * section: out [Bt][1][Hq][d] bf16, lse [Bt][1][Hq] fp32.  K <= 32,
+ * K*block < 2^30.
  */
 MSA_API msa_status msa_sparse_attn_paged_i8(const void *q, const int8_t *k_pages,
                                             const int8_t *v_pages, const float *k_scales,
