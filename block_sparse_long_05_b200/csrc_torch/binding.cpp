@@ -161,13 +161,16 @@ int rows_of(const at::Tensor &t, const char *name) {
     return static_cast<int>(t.size(0));
 }
 
-void *stream_of(PyObject *o, int device) {
+// The stream of a call: the device's current one, or the given one, which is then
+// current until the guard ends, so that the outputs' memory is its own.
+void *stream_of(PyObject *o, int device, c10::cuda::OptionalCUDAStreamGuard &guard) {
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
     PyObject *raw = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Long(o);
     if (!raw) throw PythonError();
     void *p = PyLong_AsVoidPtr(raw);
     Py_DECREF(raw);
     if (!p && PyErr_Occurred()) throw PythonError();
+    guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), static_cast<c10::DeviceIndex>(device)));
     return p;
 }
 
@@ -234,7 +237,8 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         int code = MSA_OK;
         if (total) {  // (a step without rows has nothing to write, and no pointers to check)
-            void *st = stream_of(a[3], c.device);
+            c10::cuda::OptionalCUDAStreamGuard on;
+            void *st = stream_of(a[3], c.device, on);
             const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(c.device)));
             code = i8 ? f_append_i8(k.data_ptr(), sk, v.data_ptr(), sv, x, sx, s.k.data_ptr<int8_t>(), s.v.data_ptr<int8_t>(),
                                     s.ks.data_ptr<float>(), s.vs.data_ptr<float>(), xp, p.t(), p.stride, s.pages,
@@ -261,11 +265,12 @@ PyObject *gather(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Stores s = stores(c, a + 6, i8);
         const Step p = step(c, a + 10);
         const int64_t shape[3] = {total, s.Hkv, s.d};
+        c10::cuda::OptionalCUDAStreamGuard on;
+        void *st = stream_of(a[3], c.device, on);
         const at::Tensor k = c.output(a[13], at::IntArrayRef(shape, 3), ScalarType::BFloat16, "k");
         const at::Tensor v = c.output(a[14], at::IntArrayRef(shape, 3), ScalarType::BFloat16, "v");
         int code = MSA_OK;
         if (total) {
-            void *st = stream_of(a[3], c.device);
             const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(c.device)));
             code = i8 ? f_gather_i8(s.k.const_data_ptr<int8_t>(), s.v.const_data_ptr<int8_t>(), s.ks.const_data_ptr<float>(),
                                     s.vs.const_data_ptr<float>(), p.t(), p.stride, s.pages, p.cu.const_data_ptr<int32_t>(),
@@ -294,11 +299,12 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int total = rows_of(q, "q"), Hq = static_cast<int>(q.size(1));
         const int window = integer(a[13], "window"), sinks = integer(a[14], "sinks");
         const int max_q = a[15] == Py_None ? 0 : integer(a[15], "max_q");
+        c10::cuda::OptionalCUDAStreamGuard on;
+        void *st = stream_of(a[3], c.device, on);
         const at::Tensor out = c.output(a[16], q.sizes(), ScalarType::BFloat16, "out");
         const at::Tensor lse = c.output(a[17], q.sizes().slice(0, 2), ScalarType::Float, "lse");
         int code = MSA_OK;
         if (total) {
-            void *st = stream_of(a[3], c.device);
             const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(c.device)));
             code = i8 ? f_attn_i8(q.data_ptr(), sq, s.k.const_data_ptr<int8_t>(), s.v.const_data_ptr<int8_t>(),
                                   s.ks.const_data_ptr<float>(), s.vs.const_data_ptr<float>(), p.t(), p.stride, s.pages,
@@ -329,9 +335,10 @@ PyObject *sparse(PyObject *, PyObject *const *a, Py_ssize_t n) {
             ids.size(0) != q.size(0) || ids.size(1) != 1 || ids.size(2) > INT32_MAX || table.dim() != 2 ||
             table.size(0) != q.size(0) || table.size(1) > INT32_MAX)
             throw Refused("q must be [Bt, 1, Hq, d], ids [Bt, 1, K], page_table [Bt, page_stride]");
+        c10::cuda::OptionalCUDAStreamGuard on;
+        void *st = stream_of(a[3], c.device, on);
         const at::Tensor out = c.output(a[12], q.sizes(), ScalarType::BFloat16, "out");
         const at::Tensor lse = c.output(a[13], q.sizes().slice(0, 3), ScalarType::Float, "lse");
-        void *st = stream_of(a[3], c.device);
         const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(c.device)));
         const int code = f_sparse_i8(q.data_ptr(), s.k.const_data_ptr<int8_t>(), s.v.const_data_ptr<int8_t>(),
                                      s.ks.const_data_ptr<float>(), s.vs.const_data_ptr<float>(), table.const_data_ptr<int32_t>(),

@@ -120,6 +120,16 @@ def test_many_rows_without_keys(n, count, i8):
 
 
 @pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("n, Hkv", [(1, 2), (70, 3), (300, 5), (40, 6)])
+def test_contexts_that_share_pages(n, Hkv, i8):
+    """Several contexts with the same first pages, and one page twice in a table."""
+    x = Paged([n, 5, n], [500, 450, 700], 2 * Hkv, Hkv, 64, 64, i8=i8)
+    x.table[1, :5] = x.table[0, :5]
+    x.table[2, 1] = x.table[2, 0]
+    _both(x)
+
+
+@pytest.mark.parametrize("i8", [False, True])
 @pytest.mark.parametrize("n", [1, 150])
 def test_missing_pages(n, i8):
     """Keys of a page that does not exist are left out and reported."""
@@ -324,6 +334,32 @@ def test_other_stream_and_captured_steps():
             cache_ref.check(out, lse, *want)
         assert msa.device_status(ws) == 0
         del graph
+
+
+def test_outputs_made_on_a_given_stream():
+    """Outputs of a call on a given stream do not take memory that work queued on
+    the current stream still uses."""
+    from block_sparse_long_05_b200 import msa
+    lib_ready()
+    x = Paged([1, 200], [300, 900], 8, 2, 128, 64)
+    ws = msa.Workspace.for_cache(8, 2, 128)
+    want = [t.clone() for t in _run(x, ws)]
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        torch.cuda.synchronize()
+        kept = torch.full_like(want[0], 3.0)
+        busy = torch.full((1 << 27,), 1.0, device="cuda")
+        for _ in range(20):
+            busy += 1
+        copy = kept + busy[0].to(torch.bfloat16) * 0  # reads `kept` late
+        shape = kept.shape
+        del kept  # its memory is free for the current stream only
+        got = _run(x, ws, stream=side)
+        torch.cuda.synchronize()
+        assert got[0].shape == shape
+        assert (copy == 3).all()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert msa.device_status(ws) == 0
 
 
 def test_store_past_32_bits():
