@@ -28,7 +28,8 @@
 // before this one's outputs are written.
 //
 // Measured: 2048 tokens of 32 heads over 32768 keys, bf16, d 128: 1.18 ms =
-// 0.90 PFLOP/s, 54% of a large library product, 17 us of it the merge; 8192
+// 0.90 PFLOP/s, 54% of a large library product, 17 us of it the merge (at the
+// card's power limit, 1545 MHz in a loop; 1.07 ms before it is reached); 8192
 // tokens in a window of 1024: 213 us = 0.61 PFLOP/s of visible pairs; six int8
 // contexts of up to 12007 keys with 2215 new tokens of 64 heads: 0.88 ms = 0.62
 // PFLOP/s.  A step of a row tile takes about 4100 clocks: 1700 until the scores

@@ -37,6 +37,10 @@
 //  - A producer warp keeps a ring of about 100 KB (200 KB with one CTA per
 //    SM) filled by TMA, across segment borders, and looks the pages up 32
 //    tiles at a time.
+//  - Measured: one new token of 64 heads on each of 32 int8 contexts of up to
+//    32768 keys: 176 us = 5.7 TB/s (at the card's power limit, 1605 MHz); 16
+//    selected blocks of 128 keys for each of 32: 33 us = 4.2 TB/s; one context
+//    of 4001 bf16 keys: 13 us, all of it latency.
 //  - A segment that lies in several runs leaves one fp32 piece per run, and the
 //    CTA that finishes the last piece merges them in run order.  An atomic
 //    counter tells it that it is the last; which CTA that is has no influence
