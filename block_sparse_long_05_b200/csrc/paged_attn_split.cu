@@ -18,12 +18,14 @@
 // int8 pages (k_j = code * sk_j, v_j = code * sv_j) are never converted: the
 // products are integer ones (exact), of Q and P written in 7-bit digits,
 //     q = 2^e (x2 2^14 + x1 2^7 + x0),  |x| <= 64,  e from the row's largest |q|
-//     p_j sv_j / svmax = 2^-27 (y3 2^21 + y2 2^14 + y1 2^7 + y0),  0 <= y < 128
+//     p_j sv_j = 2^(f - 27) (y3 2^21 + y2 2^14 + y1 2^7 + y0),  0 <= y < 128
 // each digit a column of its own.  q keeps 20 bits below its row's largest
-// value (a bf16 has 8 of its own); p keeps 27 bits below the row's largest so
-// far, because the many small weights beside a large one (a first token that
-// draws most of the weight) may make up the output: with 20 bits their
-// rounding would show.  sk, sv and the digits' weights are applied in fp32.  (A kernel that turned
+// value (a bf16 has 8 of its own).  2^f is the largest power of two <= the row's
+// largest p_j sv_j of the tile's 128 keys, so a term keeps 27 bits below the
+// largest one beside it: neither a V row of a large scale that this row does not
+// see or weigh, nor a key in another tile that draws most of the weight, takes
+// bits from the terms that make up the output.  sk and the digits' weights are
+// applied in fp32.  (A kernel that turned
 // the codes into bf16 fragments for mma.sync spent 700 instructions per warp
 // on 16 keys and reached 2.6 TB/s.)
 // bf16 pages take Q as it is and P as two bf16 terms (hi + lo, 16 bits).
@@ -89,6 +91,8 @@ struct Tile {
     // the ring takes what the 227 KB of an SM leave
     static constexpr int STAGES = STAGE > 32768 ? 3 : STAGE > 16384 ? (R <= 8 ? 3 : 2) : 5;
     static constexpr int COLS = 2 * (NS + NO);  // both warpgroups
+    // maxima of a warp: its rows' scores, then (int8) their weights times V scales
+    static constexpr int TW = I8 ? 2 * R : R + 4;
     static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
     static_assert(COLS <= 256, "two CTAs share the 512 columns of an SM");
 };
@@ -102,7 +106,7 @@ template <int D, bool I8, int R>
 constexpr size_t split_smem_bytes() {
     using T = Tile<D, I8, R>;
     return 1024 + static_cast<size_t>(T::STAGES) * T::STAGE + round_up(T::QBYTES, 1024) +
-           2 * round_up(T::PBYTES, 1024) + (I8 ? T::STAGES * kScaleBytes : 0) + 2 * (R + 4) * 16 + R * 36 + 16 + T::STAGES * (sizeof(StageMeta) + 16) + 72;
+           2 * round_up(T::PBYTES, 1024) + (I8 ? T::STAGES * kScaleBytes : 0) + 8 * T::TW * 4 + R * 36 + 16 + T::STAGES * (sizeof(StageMeta) + 16) + 72;
 }
 
 // Maximum over the warp (a NaN counts as absent).
@@ -252,8 +256,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
     unsigned char *q_s = ring + T::STAGES * T::STAGE;
     unsigned char *p_s = q_s + round_up(T::QBYTES, 1024);
     float *scales = reinterpret_cast<float *>(p_s + 2 * round_up(T::PBYTES, 1024));  // [stage][K, V][128]
-    static_assert(2 * round_up(T::PBYTES, 1024) >= 8192 && 8 * (R + 4) >= 64, "merge buffers");
-    constexpr int TW = R + 4;  // maxima of a warp: its rows' scores, then its V scales
+    constexpr int TW = T::TW;
+    static_assert(2 * round_up(T::PBYTES, 1024) >= 8192 && 8 * TW >= 64, "merge buffers");
     float *tops_s = scales + (I8 ? T::STAGES * 2 * kKeys : 0);     // [warp][TW]
     float *qscale = tops_s + 8 * TW;                               // [R] factor of a row's scores
     float *maxima_s = qscale + R;                                  // [warpgroup][2][R] the rows' m, tile about
@@ -561,8 +565,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                 sv = any ? scales[(2 * st + 1) * kKeys + key] : 0.f;
                 bad_sv = !(sv <= 3.4028235e38f);  // inf or NaN
                 if (bad_sv) sv = 0.f;
-                const float top = warp_max(sv);
-                if (lane == 0) tops[quarter * TW + R + (i >> 1 & 1)] = top;
             } else if (!any) {
                 // a key that no row sees counts nothing, whatever its V row holds
 #pragma unroll
@@ -614,12 +616,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
             dead = named_barrier_or(3 + wg, 128, !ok);
             if (dead) break;
             // ---- weights, relative to the running maxima
-            float svmax = 1.f, unit_sv = 1.f;
-            if (I8) {
-                const float *g = tops + R + (i >> 1 & 1);
-                svmax = fmaxf(fmaxf(g[0], g[TW]), fmaxf(g[2 * TW], g[3 * TW]));
-                unit_sv = svmax > 1e-37f ? sv * __frcp_rn(svmax) * 134217728.f : 0.f;  // 2^27 sv / svmax
-            }
             float *mnext = maxima + (m == maxima ? R : 0);
             if (key < R)
                 mnext[key] = fmaxf(fmaxf(fmaxf(tops[key], tops[TW + key]), fmaxf(tops[2 * TW + key], tops[3 * TW + key])), m[key]);
@@ -651,10 +647,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                     const float p = ex2_approx(s[r0 + e] - (mn[e] == -INFINITY ? 0.f : mn[e]));
                     l[r0 + e] += p;
                     if (I8) {
-                        const uint32_t y = __float2uint_rn(p * unit_sv);  // 2^27, at most
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            p_w[sw128_offset(k * R + r, key / 16) + key % 16] = static_cast<unsigned char>(y >> (7 * k) & 0x7Fu);
+                        s[r0 + e] = p * sv;
                     } else {
                         const __nv_bfloat16 hi = __float2bfloat16_rn(p), lo = __float2bfloat16_rn(p - __bfloat162float(hi));
                         unsigned char *at = p_w + (key / 64) * T::NO * 128 + key % 8 * 2;
@@ -664,6 +657,39 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                 }
             }
             m = mnext;
+            if (I8) {
+                // ---- digits of p sv, in units of each row's own (see the top); s[r] becomes
+                // the unit.  Units end at 2^-126: terms below 2^-99 lose bits.
+#pragma unroll
+                for (int r = 0; r < R; r += 4) {
+                    const float4 g = make_float4(warp_max(s[r]), warp_max(s[r + 1]), warp_max(s[r + 2]), warp_max(s[r + 3]));
+                    if (lane == 0) *reinterpret_cast<float4 *>(tops + quarter * TW + R + r) = g;
+                }
+                named_barrier(3 + wg, 128);
+#pragma unroll
+                for (int r0 = 0; r0 < R; r0 += 4) {
+                    float g[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const float4 x = *reinterpret_cast<const float4 *>(tops + w * TW + R + r0);
+                        g[0] = fmaxf(g[0], x.x);
+                        g[1] = fmaxf(g[1], x.y);
+                        g[2] = fmaxf(g[2], x.z);
+                        g[3] = fmaxf(g[3], x.w);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = r0 + e;
+                        // biased exponent f + 127 of the largest term, which is below 2^(f + 1)
+                        const uint32_t f = max(__float_as_uint(g[e]) & 0x7F800000u, 28u << 23);
+                        const uint32_t y = __float2uint_rn(s[r] * __uint_as_float((281u << 23) - f));  // below 2^28
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            p_w[sw128_offset(k * R + r, key / 16) + key % 16] = static_cast<unsigned char>(y >> (7 * k) & 0x7Fu);
+                        s[r] = __uint_as_float(f - (27u << 23));
+                    }
+                }
+            }
             fence_proxy_async_smem();
             tc_fence_before();
             mbar_arrive(p_ready + wg);
@@ -671,7 +697,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
             ok = mbar_wait(bar_o + wg, i >> 1 & 1, abort_flag, a.status) && ok;
             __syncwarp();
             tc_fence_after();
-            const float unit = svmax * 7.450580596923828e-9f;  // 2^-27
 #pragma unroll
             for (int r0 = 0; r0 < R; r0 += 4) {
                 uint32_t w[I8 ? 4 : 2][4];
@@ -680,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                 tmem_wait_ld();
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    o[r0 + r] = I8 ? fmaf(from_digits(w[0][r], w[1][r], w[2 * I8][r] + 128 * w[3 * I8][r]), unit, o[r0 + r])
+                    o[r0 + r] = I8 ? fmaf(from_digits(w[0][r], w[1][r], w[2 * I8][r] + 128 * w[3 * I8][r]), s[r0 + r], o[r0 + r])
                                    : o[r0 + r] + (__uint_as_float(w[0][r]) + __uint_as_float(w[1][r]));
             }
         }
