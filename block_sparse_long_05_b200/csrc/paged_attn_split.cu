@@ -28,7 +28,8 @@
 // applied in fp32.  (A kernel that turned
 // the codes into bf16 fragments for mma.sync spent 700 instructions per warp
 // on 16 keys and reached 2.6 TB/s.)
-// bf16 pages take Q as it is and P as two bf16 terms (hi + lo, 16 bits).
+// bf16 pages take Q as it is and P as two bf16 terms (hi + lo, 15 bits), both
+// positive: an infinite value of V times either of them is that infinity.
 //
 //  - The key tiles of all (sequence, row tile, kv head) segments form one
 //    list that is cut into equal runs, one per CTA: a batch with contexts of
@@ -649,7 +650,10 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                     if (I8) {
                         s[r0 + e] = p * sv;
                     } else {
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(p), lo = __float2bfloat16_rn(p - __bfloat162float(hi));
+                        // hi: the largest bf16 below p (0 for 0, so that masked keys are zeros)
+                        const uint32_t u = __float_as_uint(p), h = (u - (u != 0)) & 0xFFFF0000u;
+                        const __nv_bfloat16 hi = __ushort_as_bfloat16(static_cast<unsigned short>(h >> 16));
+                        const __nv_bfloat16 lo = __float2bfloat16_rn(p - __uint_as_float(h));
                         unsigned char *at = p_w + (key / 64) * T::NO * 128 + key % 8 * 2;
                         *reinterpret_cast<__nv_bfloat16 *>(at + sw128_offset(r, key % 64 / 8)) = hi;
                         *reinterpret_cast<__nv_bfloat16 *>(at + sw128_offset(R + r, key % 64 / 8)) = lo;

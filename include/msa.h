@@ -304,7 +304,8 @@ MSA_API msa_status msa_kv_gather_i8(const int8_t *k_pages, const int8_t *v_pages
  * chooses between kernels and changes no result beyond rounding.
  * Cache rows at or past kv_len[b], and rows that no row of the step sees, do
  * not matter, whatever they hold.  A key that one row of the step sees and
- * another does not must have finite values in v_pages (bf16).
+ * another does not must have finite values in v_pages (bf16); an infinity on a
+ * key that every row sees reaches the outputs as it is.
  */
 MSA_API msa_status msa_attn_paged(const void *q, int64_t q_stride, const void *k_pages,
                                   const void *v_pages, const int32_t *page_table, int page_stride,

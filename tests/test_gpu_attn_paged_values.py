@@ -1,0 +1,55 @@
+"""Values of V at the ends of their range: infinities on keys that every query
+sees."""
+import pytest
+import torch
+
+import cache_bounds
+import cache_ref
+from cache_ref import Paged
+from gpu_helpers import lib_ready
+
+pytestmark = pytest.mark.gpu
+
+
+def _run(x):
+    from block_sparse_long_05_b200 import msa
+    lib_ready()
+    ws = msa.Workspace.for_cache(x.Hq, x.Hkv, x.d)
+    call = msa.attn_paged_i8 if x.i8 else msa.attn_paged
+    out, lse = call(x.q, *x.stores(), *x.step(), ws)
+    assert msa.device_status(ws) == 0
+    return out, lse
+
+
+@pytest.mark.parametrize("n, kernel", [(1, "split"), (4, "split"), (1000, "chunk")])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("keys", [1, 2, 700])
+def test_infinities_that_every_row_sees(n, kernel, d, keys):
+    """A column with an infinity is that infinity, with a NaN or both infinities
+    NaN, and the other columns are what they are without them.  With one key
+    its weight is 1, a single bf16 term."""
+    x = Paged([n], [n - 1 + keys], 4, 2, d, 64)
+    k, v = x.context(0)
+    seen = cache_bounds.visible(n, x.ts[0])
+    want = [cache_bounds.reference(x, 0, 0, h, seen, kernel) for h in range(4)]
+    p = int(x.table[0, 0])
+    x.vp[p, 0, :, 3] = float("inf")
+    x.vp[p, 0, :, 7] = -float("inf")
+    x.vp[p, 0, :, 20] = float("nan")
+    x.vp[p, 0, :, 40] = float("inf")
+    both = keys > 1
+    if both:
+        x.vp[p, 1, :, 40] = -float("inf")
+        if n > 1:
+            seen2 = seen[:, 1]
+            assert seen2.all()
+    out, lse = _run(x)
+    assert (out[..., 3] == float("inf")).all()
+    assert (out[..., 7] == -float("inf")).all()
+    assert torch.isnan(out[..., 20]).all()
+    assert torch.isnan(out[..., 40]).all() if both else (out[..., 40] == float("inf")).all()
+    fine = torch.ones(d, dtype=torch.bool)
+    fine[[3, 7, 20, 40]] = False
+    for h in range(4):
+        o, l, t_out, t_lse = want[h]
+        cache_ref.check(out[:, h][:, fine], lse[:, h], o[:, fine], l, t_out[:, fine], t_lse, f"head {h}")
