@@ -65,7 +65,7 @@ __device__ __forceinline__ int seq_work(const PagedAttn &a, const Seq &s, int ov
 }
 
 // Row tile rt of a sequence: positions of its rows and its key tiles.  Tile
-// x is at key (x < na ? x : x + skip) * 64, for x < count.
+// x is at key (x < na ? x : x + skip) * 128, for x < count.
 struct RowTile {
     int r0;          // first row
     int rows;        // rows of the sequence
@@ -90,7 +90,8 @@ __device__ __forceinline__ RowTile row_tile(const PagedAttn &a, const Seq &s, in
         const int lo = max(t.tmin - a.window + 1, 0) / kKeys;
         t.na = min((min(a.sinks, max(end, 0)) + kKeys - 1) / kKeys, lo);
         t.skip = lo - t.na;
-        t.count = max(t.count - t.skip, 0);
+        // (a window may begin behind the last key that the page table holds)
+        t.count = t.na + max(t.count - lo, 0);
     }
     return t;
 }
