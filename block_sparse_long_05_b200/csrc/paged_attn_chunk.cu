@@ -13,7 +13,8 @@
 // two passes of 32 scores (first the maximum, then the weights), and takes no
 // shuffles.  The running reference m may lag behind the maximum, since weights
 // and sums are floating point numbers: it is raised, and O rescaled, only when
-// a score passes it by 2^32, which one vote per tile finds out.
+// a score passes it by 2^8, which one vote per tile finds out.  (Weights are
+// 256 at most, so that values of V up to 2^100 stay in the range of fp32.)
 //
 // int8 pages: eight warps turn the codes into bf16 tiles (exact) ahead of the
 // products; the scales sk multiply the scores and sv the weights in fp32.
@@ -65,6 +66,7 @@ constexpr int kOver = 4;       // a segment's start and end cost about as much a
 constexpr int kMinRun = 5;     // units per run, at least
 constexpr int kMetaSlots = 8;  // tiles whose positions and scales are kept: more than
                                // the rings of K and V tiles hold at a time
+constexpr float kLag = 8.f;    // powers of two by which a weight may pass 1
 constexpr float kLn2f = 0.6931471805599453f;
 
 template <int D, bool I8>
@@ -568,8 +570,8 @@ __global__ void __launch_bounds__(Chunk<D, I8>::THREADS, 1) chunk_attn_kernel(
             g *= a.scale_log2;
             // Weights and sums are floating point numbers, so the reference m may lag
             // behind the maximum: it is raised (with O and l) when a score of some row of
-            // the tile passes it by 2^32, and at first.
-            if (named_barrier_or(3 + t, 256, g > m + 32.f || !ok)) {
+            // the tile passes it by 2^kLag, and at first.
+            if (named_barrier_or(3 + t, 256, g > m + kLag || !ok)) {
                 *mine_x = g;
                 named_barrier(3 + t, 256);
                 const float mn = fmaxf(m, fmaxf(g, *other_x));

@@ -1,5 +1,6 @@
 """Values of V at the ends of their range: infinities on keys that every query
-sees."""
+sees, and finite values so large that a weight above 1 would carry them out of
+the range of fp32."""
 import pytest
 import torch
 
@@ -53,3 +54,35 @@ def test_infinities_that_every_row_sees(n, kernel, d, keys):
     for h in range(4):
         o, l, t_out, t_lse = want[h]
         cache_ref.check(out[:, h][:, fine], lse[:, h], o[:, fine], l, t_out[:, fine], t_lse, f"head {h}")
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("n, kernel", [(1, "split"), (2, "split"), (40, "chunk")])
+def test_large_values_under_scores_that_climb(n, kernel, i8):
+    """V of 2^100 and scores that climb by 20 (29 powers of two) over each context:
+    the outputs are below 2^103.  So many contexts that most are walked from the
+    first key to the last by one CTA."""
+    T, Bt, Hq = 1440, 40, 16
+    x = Paged([n] * Bt, [T] * Bt, Hq, 2, 128, 128, i8=i8)
+    x.q[..., 0] = 8
+    climb = torch.linspace(0, 20 * 128 ** 0.5 / 8, T).to(torch.bfloat16)
+    for b in range(Bt):
+        for j in range(-(-T // 128)):
+            lo, hi = j * 128, min((j + 1) * 128, T)
+            p = int(x.table[b, j])
+            k = x.k[b][lo:hi] / 4
+            k[..., 0] = climb[lo:hi, None]
+            if i8:
+                codes, sc = cache_ref.quantise(k)
+                x.kp[p, :hi - lo], x.ks[p, :, :hi - lo] = codes.cuda(), sc.t().cuda()
+                x.vs[p, :, :hi - lo] *= 2.0 ** 100
+            else:
+                x.kp[p, :hi - lo] = k.cuda()
+                x.vp[p, :hi - lo] *= 2.0 ** 100
+    out, lse = _run(x)
+    seen = cache_bounds.visible(n, T)
+    for b in range(Bt):
+        for h in range(Hq):
+            at = b * n
+            want = cache_bounds.reference(x, b, at, h, seen, kernel)
+            cache_ref.check(out[at:at + n, h], lse[at:at + n, h], *want, f"sequence {b} head {h}")
