@@ -4,11 +4,13 @@ _msa_torch.so, the compiled binding of its paged-cache calls.
 Run ``python -m block_sparse_long_05_b200.build`` or call ``build()``.  The
 shared objects are written next to this file (in-tree).  libmsa has the CUDA
 runtime linked statically, so it loads on any machine with an NVIDIA driver;
-the binding belongs to the torch and Python it was built with.
+the binding belongs to the torch and Python it was built with (recorded in
+_msa_torch.json beside it), and is built anew under others.
 """
 from __future__ import annotations
 
 import glob
+import json
 import os
 import subprocess
 import sys
@@ -19,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmsa.so")
 BINDING = os.path.join(HERE, "_msa_torch.so")
+BINDING_KEY = os.path.join(HERE, "_msa_torch.json")
 BINDING_SRC = os.path.join(HERE, "csrc_torch", "binding.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
@@ -48,9 +51,16 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every .cu under csrc/ into libmsa.so (sm_100a), and the binding.
+    """Compile every .cu under csrc/ into libmsa.so (sm_100a), then the binding
+    (which needs a C++ compiler and the headers of Python and torch; the library does not).
     Returns the library's path."""
+    build_library(force, verbose, ptxas_info)
     build_binding(force, verbose)
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Compile every .cu under csrc/ into libmsa.so (sm_100a).  Returns its path."""
     if not force and not ptxas_info and up_to_date():
         return LIB
     objs = []
@@ -79,10 +89,27 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     return LIB
 
 
+def _binding_key() -> dict:
+    """What the binding's binary interface depends on, beside its source."""
+    import torch
+    return {"torch": torch.__version__, "cxx11_abi": bool(torch._C._GLIBCXX_USE_CXX11_ABI),
+            "python": sysconfig.get_config_var("SOABI")}
+
+
+def _recorded_key():
+    try:
+        with open(BINDING_KEY) as f:
+            return json.load(f)
+    except (OSError, ValueError):
+        return None
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc_torch/binding.cpp into _msa_torch.so.  Returns the path."""
+    """Compile csrc_torch/binding.cpp into _msa_torch.so, unless it is newer than its
+    sources and was built with this torch and Python.  Returns the path."""
     header = os.path.join(ROOT, "include", "msa.h")
-    if not force and os.path.exists(BINDING) and all(
+    key = _binding_key()
+    if not force and os.path.exists(BINDING) and _recorded_key() == key and all(
             os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in (BINDING_SRC, header, __file__)):
         return BINDING
     import torch
@@ -102,7 +129,12 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
+    if os.path.exists(BINDING_KEY):  # (the record never speaks for a module that it does not belong to)
+        os.remove(BINDING_KEY)
     os.replace(tmp, BINDING)
+    with open(tmp, "w") as f:
+        json.dump(key, f)
+    os.replace(tmp, BINDING_KEY)
     return BINDING
 
 
