@@ -161,6 +161,41 @@ bool store_map(CUtensorMap *m, const void *pages, int num_pages, int block, int 
                      i8 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Which kernels take a step: the split one, the chunk one, or in a batch the
+// chunk kernel the sequences with more than kSplitMaxRows rows (tokens * G) and
+// the split kernel the others.  It depends on these sizes alone, and only on
+// those that the host knows; the lengths are in device memory.
+struct Choice {
+    bool chunk;
+    int rows;         // rows of a sequence and kv head, for the split kernel
+    long long tiles;  // row tiles of the split kernel, at most
+    long long keys;   // key tiles of a row tile, at most
+};
+// max_q: rows of the longest sequence, as far as the caller knows.  span: keys
+// of a context, as wide as its page-table row (or the selected blocks).
+Choice choose(int Bt, int total, int max_q, int G, int Hkv, long long span, int window, int sinks,
+              bool sparse) {
+    Choice c;
+    // (a hint below the average is wrong)
+    const long long mean = (static_cast<long long>(total) + Bt - 1) / Bt;
+    const long long most = (max_q > mean ? max_q : mean) * G;
+    c.rows = most <= kSplitMaxRows ? static_cast<int>(most) : kSplitMaxRows + 1;
+    c.keys = span / kSplitKeys + 1;
+    const long long near = (static_cast<long long>(window) + sinks) / kSplitKeys + 4;
+    if (window && c.keys > near) c.keys = near;
+    c.tiles = static_cast<long long>(total) * G / kSplitMaxRows + Bt;
+    // Sequences with many rows go to the chunk kernel, unless the whole step is
+    // small: it takes 14 us or more where the split kernel, 16 rows at a time, has
+    // done with a few hundred tiles.  Measured with page tables as wide as the
+    // contexts (bf16, d 128, G 4; split against chunk): 64 rows over 500 keys, 8 kv
+    // heads: 14 / 23 us; 20 over 2000: 26 / 27; 200 over 200: 21 / 20; 500 over 500,
+    // 2 kv heads: 18 / 24, 8 kv heads: 53 / 25; 64 over 4000: 45 / 38.  (Behind a wider
+    // table the same contexts count as longer ones, and their steps go to the chunk
+    // kernel earlier.)  A hint that is too low costs time, not rows.
+    c.chunk = c.rows > kSplitMaxRows && !sparse && c.tiles * Hkv * (c.keys + 2) > 1536;
+    return c;
+}
+
 // Shared by the dense and the sparse entry: `a` has everything but the
 // workspace regions and the scale of the scores.
 // max_q: rows of the longest sequence, as far as the caller knows.
@@ -197,30 +232,16 @@ msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int nu
         !store_map(&tv, v_pages, num_pages, a.step.block, a.c.Hkv, a.c.d, box, i8))
         return MSA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // (a hint below the average is wrong)
-    const long long mean = (static_cast<long long>(a.step.total) + a.step.Bt - 1) / a.step.Bt;
-    const long long most = (max_q > mean ? max_q : mean) * a.G;
-    const int rows = most <= kSplitMaxRows ? static_cast<int>(most) : kSplitMaxRows + 1;
-    // the most row tiles and key tiles that the step may have
-    const long long all = static_cast<long long>(a.step.total) * a.G;
     const long long span = a.ids ? static_cast<long long>(a.K) * a.step.block
                                  : static_cast<long long>(a.step.pm.stride) * a.step.block;
-    long long keys = span / kSplitKeys + 1;
-    const long long near = (static_cast<long long>(a.window) + a.sinks) / kSplitKeys + 4;
-    if (a.window && keys > near) keys = near;
-    const long long tiles = all / kSplitMaxRows + a.step.Bt;
-    // Sequences with many rows go to the chunk kernel, unless the whole step is
-    // small: it takes 14 us or more where the split kernel, 16 rows at a time, has
-    // done with a few hundred tiles.  Measured (bf16, d 128, G 4; split against
-    // chunk): 64 rows over 500 keys, 8 kv heads: 14 / 23 us; 20 over 2000: 26 / 27;
-    // 200 over 200: 21 / 20; 500 over 500, 2 kv heads: 18 / 24, 8 kv heads:
-    // 53 / 25; 64 over 4000: 45 / 38.  In a batch the split kernel then takes the
-    // sequences with few rows; a hint that is too low costs time, not rows.
-    const bool chunk = rows > kSplitMaxRows && !a.ids && tiles * a.c.Hkv * (keys + 2) > 1536;
+    const Choice how = choose(a.step.Bt, a.step.total, max_q, a.G, a.c.Hkv, span, a.window, a.sinks,
+                              a.ids != nullptr);
+    const bool chunk = how.chunk;
     share(chunk ? sms : 0);
     // work units are numbered with 31 bits
-    const long long row_tiles = chunk ? all / kChunkRows + 2ll * a.step.Bt : 2 * tiles;
-    if (row_tiles * a.groups * (keys + 8) >= (1ll << 31)) return MSA_ERR_UNSUPPORTED;
+    const long long all = static_cast<long long>(a.step.total) * a.G;
+    const long long row_tiles = chunk ? all / kChunkRows + 2ll * a.step.Bt : 2 * how.tiles;
+    if (row_tiles * a.groups * (how.keys + 8) >= (1ll << 31)) return MSA_ERR_UNSUPPORTED;
     cudaError_t e = cudaSuccess;
     if (chunk) {
         a.row_lo = a.step.Bt > 1 ? kSplitMaxRows + 1 : 0;
@@ -230,9 +251,15 @@ msa_status attend(PagedAttn &a, const void *k_pages, const void *v_pages, int nu
         share(0);
     }
     if (e == cudaSuccess && (!chunk || a.step.Bt > 1))
-        e = launch_split_attn(a, rows, tk, tv, sms, st);
+        e = launch_split_attn(a, how.rows, tk, tv, sms, st);
     return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
+
+// (positions stay below 2^30, so a longer window hides nothing)
+int clamp_window(int window) { return window < (1 << 30) ? window : 1 << 30; }
+int clamp_sinks(int window, int sinks) { return !window ? 0 : sinks < (1 << 30) ? sinks : 1 << 30; }
+// Without a hint one sequence may have all the rows.
+int known_rows(int max_q, int total) { return max_q > 0 && max_q < total ? max_q : total; }
 
 msa_status attn_impl(const void *q, int64_t q_stride, const void *k_pages, const void *v_pages,
                      const float *k_scales, const float *v_scales, const int32_t *page_table,
@@ -264,10 +291,9 @@ msa_status attn_impl(const void *q, int64_t q_stride, const void *k_pages, const
     a.lse = lse;
     a.Hq = Hq;
     a.G = Hq / Hkv;
-    // positions stay below 2^30, so a longer window hides nothing
-    a.window = window < (1 << 30) ? window : 1 << 30;
-    a.sinks = !window ? 0 : sinks < (1 << 30) ? sinks : 1 << 30;
-    return attend(a, k_pages, v_pages, num_pages, max_q > 0 && max_q < total ? max_q : total, ws, stream);
+    a.window = clamp_window(window);
+    a.sinks = clamp_sinks(window, sinks);
+    return attend(a, k_pages, v_pages, num_pages, known_rows(max_q, total), ws, stream);
 }
 
 }  // namespace
@@ -319,6 +345,17 @@ msa_status msa_kv_gather_i8(const int8_t *k_pages, const int8_t *v_pages, const 
     return gather_impl(k_pages, v_pages, k_scales, v_scales, page_table, page_stride, num_pages,
                        cu, kv_len, k, v, Bt, total, Hkv, d, block, workspace, workspace_bytes,
                        stream, true);
+}
+
+int msa_attn_paged_kernels(int Bt, int total, int max_q, int Hq, int Hkv, int block,
+                           int page_stride, int window, int sinks) {
+    if (Bt < 1 || total < 1 || max_q < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || block < 1 ||
+        page_stride < 1 || window < 0 || sinks < 0)
+        return 0;
+    const Choice c = choose(Bt, total, known_rows(max_q, total), Hq / Hkv, Hkv,
+                            static_cast<long long>(page_stride) * block, clamp_window(window),
+                            clamp_sinks(window, sinks), false);
+    return (!c.chunk || Bt > 1 ? MSA_KERNEL_SPLIT : 0) | (c.chunk ? MSA_KERNEL_CHUNK : 0);
 }
 
 msa_status msa_attn_paged(const void *q, int64_t q_stride, const void *k_pages,

@@ -32,7 +32,7 @@ EXPORTED = ("msa_workspace_size", "msa_index_topk", "msa_select_invert", "msa_sp
             "msa_sparse_attn_paged", "msa_index_topk_i8", "msa_index_topk_i8_ev",
             "msa_workspace_size_kv_group", "msa_cache_workspace_size", "msa_kv_append",
             "msa_kv_append_i8", "msa_kv_gather", "msa_kv_gather_i8", "msa_attn_paged",
-            "msa_attn_paged_i8", "msa_sparse_attn_paged_i8")
+            "msa_attn_paged_i8", "msa_sparse_attn_paged_i8", "msa_attn_paged_kernels")
 
 MAX_STAGES = 4
 
@@ -124,6 +124,8 @@ def load_library(path: str = LIB_PATH):
     for f in ("kv_append", "kv_append_i8", "kv_gather", "kv_gather_i8", "attn_paged",
               "attn_paged_i8", "sparse_attn_paged_i8"):
         getattr(lib, "msa_" + f).restype = I
+    lib.msa_attn_paged_kernels.argtypes = [I] * 9
+    lib.msa_attn_paged_kernels.restype = I
     lib.msa_selftest_umma.argtypes = [P, P, P, I, I, I, P, P]
     lib.msa_selftest_umma.restype = I
     _lib = lib
@@ -474,6 +476,15 @@ def attn_paged_i8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     if r.__class__ is int:
         raise MSAError("msa_attn_paged_i8", r)
     return r
+
+
+def attn_paged_kernels(Bt: int, total: int, Hq: int, Hkv: int, block: int, page_stride: int,
+                       window: int = 0, sinks: int = 0, max_q: int | None = None) -> tuple[str, ...]:
+    """The kernels that attn_paged and attn_paged_i8 launch for a step of these sizes
+    (msa_attn_paged_kernels): "split", "chunk", both, or none."""
+    m = load_library().msa_attn_paged_kernels(Bt, total, max_q or 0, Hq, Hkv, block, page_stride,
+                                              window, sinks)
+    return tuple(name for bit, name in ((1, "split"), (2, "chunk")) if m & bit)
 
 
 def sparse_attn_paged_i8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,

@@ -324,6 +324,18 @@ MSA_API msa_status msa_attn_paged_i8(const void *q, int64_t q_stride, const int8
                                      size_t workspace_bytes, void *stream);
 
 /*
+ * The kernels that msa_attn_paged and msa_attn_paged_i8 launch for a step of
+ * these sizes (profiling and tests): MSA_KERNEL_SPLIT, MSA_KERNEL_CHUNK or both,
+ * where the chunk kernel takes the sequences with more than 16 rows (n_b * Hq /
+ * Hkv) and the split kernel the others; 0 for sizes without work or that the
+ * calls reject.  Host only: no CUDA call is made.
+ */
+#define MSA_KERNEL_SPLIT 1
+#define MSA_KERNEL_CHUNK 2
+MSA_API int msa_attn_paged_kernels(int Bt, int total, int max_q, int Hq, int Hkv, int block,
+                                   int page_stride, int window, int sinks);
+
+/*
  * The sparse branch of a decode step on int8 pages: msa_sparse_attn_paged
  * (same ids, same keys) with the 8-bit stores and the output types of this
  * section: out [Bt][1][Hq][d] bf16, lse [Bt][1][Hq] fp32.  K <= 32,

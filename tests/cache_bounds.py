@@ -13,6 +13,18 @@ import torch
 from cache_ref import BF16, attend
 
 
+def reaches(x, kernel, window=0, sinks=0, max_q=None):
+    """Whether attention over the batch x takes that kernel, "split" or "chunk", for
+    its longest sequence.  (Where both are launched, the split kernel has the
+    sequences of at most 16 rows per kv head.)"""
+    from block_sparse_long_05_b200 import msa
+    taken = msa.attn_paged_kernels(len(x.ns), x.q.shape[0], x.Hq, x.Hkv, x.block, x.table.shape[1],
+                                   window, sinks, max_q)
+    if len(taken) == 2:
+        taken = ("chunk",) if max(x.ns) * x.Hq // x.Hkv > 16 else ("split",)
+    return taken == (kernel,)
+
+
 def visible(n, t, window=0, sinks=0, cap=None, device="cuda"):
     """Keys [n, cap or t] that the n rows at positions t - n .. t - 1 see."""
     i = torch.arange(t - n, t, device=device)[:, None]

@@ -18,6 +18,7 @@ ROWS = [(1, "split"), (4, "split"), (1000, "chunk")]
 def _check(x, kernel, ws=None):
     from block_sparse_long_05_b200 import msa
     lib_ready()
+    assert cache_bounds.reaches(x, kernel)
     ws = ws or msa.Workspace.for_cache(x.Hq, x.Hkv, x.d)
     out, lse = msa.attn_paged_i8(x.q, *x.stores(), *x.step(), ws)
     assert msa.device_status(ws) == 0

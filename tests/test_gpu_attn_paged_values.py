@@ -12,9 +12,10 @@ from gpu_helpers import lib_ready
 pytestmark = pytest.mark.gpu
 
 
-def _run(x):
+def _run(x, kernel):
     from block_sparse_long_05_b200 import msa
     lib_ready()
+    assert cache_bounds.reaches(x, kernel)
     ws = msa.Workspace.for_cache(x.Hq, x.Hkv, x.d)
     call = msa.attn_paged_i8 if x.i8 else msa.attn_paged
     out, lse = call(x.q, *x.stores(), *x.step(), ws)
@@ -44,7 +45,7 @@ def test_infinities_that_every_row_sees(n, kernel, d, keys):
         if n > 1:
             seen2 = seen[:, 1]
             assert seen2.all()
-    out, lse = _run(x)
+    out, lse = _run(x, kernel)
     assert (out[..., 3] == float("inf")).all()
     assert (out[..., 7] == -float("inf")).all()
     assert torch.isnan(out[..., 20]).all()
@@ -79,7 +80,7 @@ def test_large_values_under_scores_that_climb(n, kernel, i8):
             else:
                 x.kp[p, :hi - lo] = k.cuda()
                 x.vp[p, :hi - lo] *= 2.0 ** 100
-    out, lse = _run(x)
+    out, lse = _run(x, kernel)
     seen = cache_bounds.visible(n, T)
     for b in range(Bt):
         for h in range(Hq):

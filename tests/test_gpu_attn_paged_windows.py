@@ -24,6 +24,7 @@ def test_window_of_a_context_longer_than_its_table(n, kv_len, sinks, i8):
     x = Paged([n], [cap], 8, 2, 128, 64, i8=i8)
     x.table = x.table[:, :10].contiguous()
     x.kv_len = torch.tensor([kv_len], dtype=torch.int32, device="cuda")
+    assert cache_bounds.reaches(x, "chunk" if n == 600 else "split", window, sinks)
     ws = msa.Workspace.for_cache(8, 2, 128)
     call = msa.attn_paged_i8 if i8 else msa.attn_paged
     out, lse = call(x.q, *x.stores(), *x.step(), ws, window=window, sinks=sinks)
