@@ -24,10 +24,14 @@
 // largest p_j sv_j of the tile's 128 keys, so a term keeps 27 bits below the
 // largest one beside it: neither a V row of a large scale that this row does not
 // see or weigh, nor a key in another tile that draws most of the weight, takes
-// bits from the terms that make up the output.  sk and the digits' weights are
-// applied in fp32.  (A kernel that turned
-// the codes into bf16 fragments for mma.sync spent 700 instructions per warp
-// on 16 keys and reached 2.6 TB/s.)
+// bits from the terms that make up the output.  Where the tile's scales lie
+// within a factor of 4, as they mostly do, 2^f comes from the row's largest p and
+// the largest scale, and a term keeps 23 bits or more; else the warps exchange
+// the terms' maxima (in every tile: 192 us instead of 184 on the decode step
+// below, and 354 instead of 297 with 16 rows per tile).  sk and the digits'
+// weights are applied in fp32.  (A kernel that turned the codes into bf16
+// fragments for mma.sync spent 700 instructions per warp on 16 keys and reached
+// 2.6 TB/s.)
 // bf16 pages take Q as it is and P as two bf16 terms (hi + lo, 15 bits), both
 // positive: an infinite value of V times either of them is that infinity.
 //
@@ -40,10 +44,11 @@
 //  - A producer warp keeps a ring of about 100 KB (200 KB with one CTA per
 //    SM) filled by TMA, across segment borders, and looks the pages up 32
 //    tiles at a time.
-//  - Measured: one new token of 64 heads on each of 32 int8 contexts of up to
-//    32768 keys: 176 us = 5.7 TB/s (at the card's power limit, 1605 MHz); 16
-//    selected blocks of 128 keys for each of 32: 33 us = 4.2 TB/s; one context
-//    of 4001 bf16 keys: 13 us, all of it latency.
+//  - Measured, in a replayed graph: one new token of 64 heads on each of 32
+//    int8 contexts of up to 32768 keys: 184 us = 5.4 TB/s (at the card's power
+//    limit), on bf16 ones 302 us = 6.4 TB/s; 16 selected blocks of 128 keys for
+//    each of 32: 33 us = 4.2 TB/s; one context of 4001 bf16 keys: 12.7 us, all of
+//    it latency.
 //  - A segment that lies in several runs leaves one fp32 piece per run, and the
 //    CTA that finishes the last piece merges them in run order.  An atomic
 //    counter tells it that it is the last; which CTA that is has no influence
@@ -92,8 +97,9 @@ struct Tile {
     // the ring takes what the 227 KB of an SM leave
     static constexpr int STAGES = STAGE > 32768 ? 3 : STAGE > 16384 ? (R <= 8 ? 3 : 2) : 5;
     static constexpr int COLS = 2 * (NS + NO);  // both warpgroups
-    // maxima of a warp: its rows' scores, then (int8) their weights times V scales
-    static constexpr int TW = I8 ? 2 * R : R + 4;
+    // maxima of a warp: its rows' scores, then (int8) their weights times V scales, and
+    // the least and largest of its V scales, of two tiles
+    static constexpr int TW = I8 ? 2 * R + 4 : R + 4;
     static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
     static_assert(COLS <= 256, "two CTAs share the 512 columns of an SM");
 };
@@ -106,14 +112,19 @@ constexpr int kScaleBytes = 2 * kKeys * 4;  // K and V scales of a stage
 template <int D, bool I8, int R>
 constexpr size_t split_smem_bytes() {
     using T = Tile<D, I8, R>;
-    return 1024 + static_cast<size_t>(T::STAGES) * T::STAGE + round_up(T::QBYTES, 1024) +
+    return static_cast<size_t>(T::STAGES) * T::STAGE + round_up(T::QBYTES, 1024) +
            2 * round_up(T::PBYTES, 1024) + (I8 ? T::STAGES * kScaleBytes : 0) + 8 * T::TW * 4 + R * 36 + 16 + T::STAGES * (sizeof(StageMeta) + 16) + 72;
 }
 
-// Maximum over the warp (a NaN counts as absent).
+// Maximum and minimum over the warp (a NaN counts as absent).
 __device__ __forceinline__ float warp_max(float x) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float warp_min(float x) {
+    float r;
+    asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
 
@@ -251,9 +262,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __grid_constant__ PagedAttn a) {
     using T = Tile<D, I8, R>;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *ring = reinterpret_cast<unsigned char *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) unsigned char ring[];
     unsigned char *q_s = ring + T::STAGES * T::STAGE;
     unsigned char *p_s = q_s + round_up(T::QBYTES, 1024);
     float *scales = reinterpret_cast<float *>(p_s + 2 * round_up(T::PBYTES, 1024));  // [stage][K, V][128]
@@ -566,6 +575,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                 sv = any ? scales[(2 * st + 1) * kKeys + key] : 0.f;
                 bad_sv = !(sv <= 3.4028235e38f);  // inf or NaN
                 if (bad_sv) sv = 0.f;
+                const float2 ends = make_float2(warp_min(any ? sv : INFINITY), warp_max(sv));
+                if (lane == 0) *reinterpret_cast<float2 *>(tops + quarter * TW + 2 * R + (i & 2)) = ends;
             } else if (!any) {
                 // a key that no row sees counts nothing, whatever its V row holds
 #pragma unroll
@@ -617,23 +628,47 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
             dead = named_barrier_or(3 + wg, 128, !ok);
             if (dead) break;
             // ---- weights, relative to the running maxima
+            // int8: V scales within a factor of 4 (the same for all), and the largest one's exponent
+            bool alike = false;
+            int top_sv = 0;
+            if (I8) {
+                float lo = INFINITY, hi = 0.f;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float2 ends = *reinterpret_cast<const float2 *>(tops + w * TW + 2 * R + (i & 2));
+                    lo = fminf(lo, ends.x);
+                    hi = fmaxf(hi, ends.y);
+                }
+                alike = hi <= 4.f * lo;
+                top_sv = __float_as_int(hi) & 0x7F800000;
+            }
+            // digits of a term p sv of row r, in the unit 2^(f - 127 - 27 + spare) (f: in place of
+            // a float's exponent); returns the unit.  Units end at 2^-126.
+            auto digits = [&](int r, float term, int f, int spare) -> float {
+                f = max(f, 28 << 23);
+                const uint32_t y = __float2uint_rn(term * __int_as_float(((281 - spare) << 23) - f));  // below 2^28
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    p_w[sw128_offset(k * R + r, key / 16) + key % 16] = static_cast<unsigned char>(y >> (7 * k) & 0x7Fu);
+                return __int_as_float(f - ((27 - spare) << 23));
+            };
             float *mnext = maxima + (m == maxima ? R : 0);
             if (key < R)
                 mnext[key] = fmaxf(fmaxf(fmaxf(tops[key], tops[TW + key]), fmaxf(tops[2 * TW + key], tops[3 * TW + key])), m[key]);
 #pragma unroll
             for (int r0 = 0; r0 < R; r0 += 4) {
-                float mo[4], mn[4];
+                float mo[4], mn[4], mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // mt: of this tile
                 *reinterpret_cast<float4 *>(mo) = *reinterpret_cast<const float4 *>(m + r0);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mn[e] = mo[e];
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const float4 g = *reinterpret_cast<const float4 *>(tops + w * TW + r0);
-                    mn[0] = fmaxf(mn[0], g.x);
-                    mn[1] = fmaxf(mn[1], g.y);
-                    mn[2] = fmaxf(mn[2], g.z);
-                    mn[3] = fmaxf(mn[3], g.w);
+                    mt[0] = fmaxf(mt[0], g.x);
+                    mt[1] = fmaxf(mt[1], g.y);
+                    mt[2] = fmaxf(mt[2], g.z);
+                    mt[3] = fmaxf(mt[3], g.w);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mn[e] = fmaxf(mo[e], mt[e]);
                 if (mn[0] != mo[0] || mn[1] != mo[1] || mn[2] != mo[2] || mn[3] != mo[3]) {  // (the same for all)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -649,6 +684,12 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                     l[r0 + e] += p;
                     if (I8) {
                         s[r0 + e] = p * sv;
+                        if (alike) {
+                            // p <= 2^(mt - mn), so the terms are below 2^(f + 1) (one bit is spared for the
+                            // approximation of p), and the largest is not below 2^(f - 3)
+                            const float up = __fadd_ru(fmaxf(mt[e] - mn[e], -127.f), 12582912.f);  // 1.5 2^23: rounds up to an integer
+                            s[r0 + e] = digits(r, s[r0 + e], top_sv + static_cast<int>(__float_as_uint(up) << 23), 1);
+                        }
                     } else {
                         // hi: the largest bf16 below p (0 for 0, so that masked keys are zeros)
                         const uint32_t u = __float_as_uint(p), h = (u - (u != 0)) & 0xFFFF0000u;
@@ -661,9 +702,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                 }
             }
             m = mnext;
-            if (I8) {
-                // ---- digits of p sv, in units of each row's own (see the top); s[r] becomes
-                // the unit.  Units end at 2^-126: terms below 2^-99 lose bits.
+            if (I8 && !alike) {
+                // the rows' largest terms themselves
 #pragma unroll
                 for (int r = 0; r < R; r += 4) {
                     const float4 g = make_float4(warp_max(s[r]), warp_max(s[r + 1]), warp_max(s[r + 2]), warp_max(s[r + 3]));
@@ -671,27 +711,18 @@ __global__ void __launch_bounds__(kThreads, Tile<D, I8, R>::CTAS) split_attn_ker
                 }
                 named_barrier(3 + wg, 128);
 #pragma unroll
-                for (int r0 = 0; r0 < R; r0 += 4) {
+                for (int r = 0; r < R; r += 4) {
                     float g[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        const float4 x = *reinterpret_cast<const float4 *>(tops + w * TW + R + r0);
+                        const float4 x = *reinterpret_cast<const float4 *>(tops + w * TW + R + r);
                         g[0] = fmaxf(g[0], x.x);
                         g[1] = fmaxf(g[1], x.y);
                         g[2] = fmaxf(g[2], x.z);
                         g[3] = fmaxf(g[3], x.w);
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = r0 + e;
-                        // biased exponent f + 127 of the largest term, which is below 2^(f + 1)
-                        const uint32_t f = max(__float_as_uint(g[e]) & 0x7F800000u, 28u << 23);
-                        const uint32_t y = __float2uint_rn(s[r] * __uint_as_float((281u << 23) - f));  // below 2^28
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            p_w[sw128_offset(k * R + r, key / 16) + key % 16] = static_cast<unsigned char>(y >> (7 * k) & 0x7Fu);
-                        s[r] = __uint_as_float(f - (27u << 23));
-                    }
+                    for (int e = 0; e < 4; ++e) s[r + e] = digits(r + e, s[r + e], __float_as_int(g[e]) & 0x7F800000, 0);
                 }
             }
             fence_proxy_async_smem();

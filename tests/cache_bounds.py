@@ -51,9 +51,10 @@ def bounds(q, k, v, seen, kernel, sv=None):
     The split kernel on bf16 pages takes a weight as two bf16 terms: the first
     leaves at most 2^-7 of it, of which the second misses BF16, below 2^-15.
     On int8 pages the products w_j sv_j of a row and a tile of 128 keys are
-    rounded to multiples of 2^-27 of a power of two within a factor sqrt(2) of
-    the tile's largest one: by at most 2^-27 of that, for a code of at most 127.
-    Keys that the row does not see are exact zeros.
+    rounded to multiples of 2^(f - 26), where 2^(f - 3) is at most the tile's
+    largest one (the row's largest w, rounded down to a power of two, times the
+    largest sv, rounded down likewise, over 4): by at most 2^-24 of that, for a
+    code of at most 127.  Keys that the row does not see are exact zeros.
 
     The second product adds 128 keys in fp32 at a time, then keys / 128 such
     sums and their merge.  One rounding to bf16 at the end."""
@@ -70,7 +71,7 @@ def bounds(q, k, v, seen, kernel, sv=None):
     elif sv is None:
         t_out = t_out + 2.0 ** -15 * wide
     else:
-        t_out = t_out + (seen.sum(1) * 127 * 2.0 ** -27 * (w * sv).amax(1))[:, None]
+        t_out = t_out + (seen.sum(1) * 127 * 2.0 ** -24 * (w * sv).amax(1))[:, None]
     return BF16 * (w @ v).abs() + (1 + BF16) * t_out + 1e-30, t_lse
 
 

@@ -44,6 +44,9 @@ def _excess(T, form, up=0, i8=True):
             terms = part * sv[t:t + 128]
             if form == "unit of the tile":
                 unit = sv[t:t + 128].max() * 2.0 ** -27
+            elif form == "unit of the maxima":
+                unit = torch.exp2(torch.ceil(torch.log2(part.amax(1, keepdim=True))) - 26 +
+                                  torch.floor(torch.log2(sv[t:t + 128].max())))
             else:
                 unit = torch.exp2(torch.floor(torch.log2(terms.amax(1, keepdim=True))) - 27)
             x, rows = (terms / unit).round() * unit, rows / sv[t:t + 128, None]
@@ -58,6 +61,7 @@ def _excess(T, form, up=0, i8=True):
 def test_bounds_of_the_split_kernel(T):
     assert _excess(T, "two bf16 terms", i8=False) <= 1
     assert _excess(T, "bf16", i8=False) > 1
+    assert _excess(T, "unit of the maxima") <= 1
     for up in (0, 16, 20, 24, 28):
         assert _excess(T, "unit of the row", up) <= 1
     for up in (20, 24, 28):

@@ -1,5 +1,5 @@
 """The split kernel of the attention over pages keeps its weights to 15 bits (bf16
-pages) or 27 (int8 pages): the bounds are those of cache_bounds, which reject
+pages) or 23 (int8 pages): the bounds are those of cache_bounds, which reject
 weights rounded to bf16 (test_cache_bounds.py)."""
 import pytest
 import torch

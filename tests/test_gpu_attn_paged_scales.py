@@ -12,7 +12,7 @@ from gpu_helpers import lib_ready
 pytestmark = pytest.mark.gpu
 
 # rows of one sequence, and the kernel that takes them (G 2, 2 kv heads, 700 keys and more)
-ROWS = [(1, "split"), (4, "split"), (1000, "chunk")]
+ROWS = [(1, "split"), (4, "split"), (7, "split"), (1000, "chunk")]
 
 
 def _check(x, kernel, ws=None):
