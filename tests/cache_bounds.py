@@ -48,6 +48,10 @@ def bounds(q, k, v, seen, kernel, sv=None):
 
     The chunk kernel rounds each weight (times its V scale) to bf16.
 
+    On int8 pages the split kernel takes q in multiples of 2^-19 of the power of
+    two below its row's largest value: what that takes from q_i (nothing, for
+    values within 2^12 of the largest) moves a score by its product with k_i.
+
     The split kernel on bf16 pages takes a weight as two bf16 terms: the first
     leaves at most 2^-7 of it, of which the second misses BF16, below 2^-15.
     On int8 pages the products w_j sv_j of a row and a tile of 128 keys are
@@ -60,6 +64,9 @@ def bounds(q, k, v, seen, kernel, sv=None):
     sums and their merge.  One rounding to bf16 at the end."""
     w = weights(q, k, seen)
     e = (q.shape[1] + 4) * 2.0 ** -23 * (q.abs() @ k.abs().t()) / q.shape[1] ** 0.5
+    if kernel == "split" and sv is not None:
+        unit = torch.exp2(torch.floor(torch.log2(q.abs().amax(1, keepdim=True).clamp(min=1e-30))) - 19)
+        e = e + (q - (q / unit).round() * unit).abs() @ k.abs().t() / q.shape[1] ** 0.5
     of_sum = (w * e).sum(1)
     wide = w @ v.abs()
     lse = torch.logsumexp(torch.where(seen, q @ k.t() / q.shape[1] ** 0.5, torch.full_like(w, -1e300)), 1)
