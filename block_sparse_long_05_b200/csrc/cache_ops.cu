@@ -12,17 +12,19 @@
 //                  as NaN instead of as values that look sound.
 //   gather  packed bf16 rows <- code_i * scale, rounded once (int8), or a copy.
 //
-// Both are bound by HBM: bytes per value are 2 + 1 (int8) or 2 + 2 (bf16).  To
-// get there they must be lean: at 6.5 TB/s an SM has about four issue slots per
+// HBM is what bounds them at best: bytes per value are 2 + 1 (int8) or 2 + 2
+// (bf16).  To get there they must be lean: at 6.5 TB/s an SM has about four issue slots per
 // 32 values.  A thread moves units of 16 bytes of the store: 8 bf16 values, or
 // 16 codes.  Values become codes and codes values by adding a power of two
 // whose last mantissa bit counts 1, so that no conversion instruction (a quarter
 // of the rate) is needed.  The page of each token is looked up once per token of
-// the CTA's run, into shared memory.  Measured: int8 append of 24573 rows (8
-// heads, d 128) 30 us = 5.0 TB/s, int8 gather of 131072 rows 131 us = 6.2 TB/s
-// (151 us where its 32 bytes per thread are stored as two halves, as for
-// outputs that do not begin on 32 bytes; the append's loads gain nothing from
-// it, 31.5 us); one or four units of codes per thread, or pairs of lanes that
+// the CTA's run, into shared memory.  Measured: int8 append of 22190 rows (8
+// heads, d 128) 32 us = 4.7 TB/s, int8 gather of 131072 rows 134 us = 6.1 TB/s
+// in a replayed graph (151 us where its 32 bytes per thread are stored as two
+// halves, as for outputs that do not begin on 32 bytes; the append's loads gain
+// nothing from it).  The append does not get there at that size: 67% of the issue
+// slots are taken, and its warps wait longest at the barrier behind the look-up
+// of their rows.  One or four units of codes per thread, or pairs of lanes that
 // read 32 bytes side by side and exchange them in registers, were slower.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -50,7 +52,7 @@ constexpr float kMagic = 12582912.f;             // 1.5 * 2^23
 
 // The step's row offsets in shared memory, unless there are too many: a
 // search for a row's sequence is then a chain of shared-memory reads, not of
-// trips to L2 (which made an append of 24 K rows twice as long).
+// trips to L2 (which made an append of 22 K rows twice as long).
 constexpr int kSharedSeqs = 1024;
 __device__ __forceinline__ const int32_t *share_offsets(const StepMap &s, int32_t *sh) {
     if (s.Bt > kSharedSeqs) return s.cu;

@@ -19,21 +19,22 @@
 // int8 pages: eight warps turn the codes into bf16 tiles (exact) ahead of the
 // products; the scales sk multiply the scores and sv the weights in fp32.
 //
-// P is rounded to bf16 (a relative error of at most 2^-8 per weight, averaged
-// over the keys; the sum l takes the unrounded values): the output's own
-// rounding is as large, and a second term would double the second product.
+// P (with int8 pages: P times sv) is rounded to bf16, a relative error of at most
+// 2^-8 per weight, averaged over the keys; the sum l takes the unrounded values.
+// The output's own rounding is as large, and a second term would double the
+// second product.
 //
 // The work is cut into equal runs of key tiles, one CTA per SM (paged_walk.cuh).
 // Segments in several runs leave fp32 pieces that a second kernel merges.  At a
 // segment's end the next one's Q is on its way, and its first products run,
 // before this one's outputs are written.
 //
-// Measured: 2048 tokens of 32 heads over 32768 keys, bf16, d 128: 1.18 ms =
-// 0.90 PFLOP/s, 54% of a large library product, 17 us of it the merge (at the
-// card's power limit, 1545 MHz in a loop; 1.07 ms before it is reached); 8192
-// tokens in a window of 1024: 213 us = 0.61 PFLOP/s of visible pairs; six int8
-// contexts of up to 12007 keys with 2215 new tokens of 64 heads: 0.88 ms = 0.62
-// PFLOP/s.  A step of a row tile takes about 4100 clocks: 1700 until the scores
+// Measured, in a replayed graph: 2048 tokens of 32 heads over 32768 keys, bf16,
+// d 128: 1.26 ms = 0.85 PFLOP/s, 51% of a large library product, 14 us of it the
+// merge (at the card's power limit, 1540 MHz in a loop; 1.08 ms before it is
+// reached); 8192 tokens in a window of 1024: 215 us = 0.60 PFLOP/s of visible
+// pairs (int8: 334 us); six int8 contexts of up to 12007 keys with 2215 new
+// tokens of 64 heads: 0.88 ms = 0.62 PFLOP/s.  A step of a row tile takes about 4100 clocks: 1700 until the scores
 // of the next 128 keys are there (its own two products and the other tile's,
 // 512 clocks each, and the way there), 500 for the maximum, 150 for the vote,
 // 1450 for the weights.  S and P share columns, and with O they fill tensor

@@ -20,7 +20,9 @@
 //     q = 2^e (x2 2^14 + x1 2^7 + x0),  |x| <= 64,  e from the row's largest |q|
 //     p_j sv_j = 2^(f - 27) (y3 2^21 + y2 2^14 + y1 2^7 + y0),  0 <= y < 128
 // each digit a column of its own.  q keeps 20 bits below its row's largest
-// value (a bf16 has 8 of its own).  2^f is the largest power of two <= the row's
+// value: a bf16 has 8 of its own, so values within 2^12 of the largest are exact,
+// and what smaller ones lose moves a score by at most 2^-20 max |q_i| sum |k_i| /
+// sqrt(d), 1/32 of what the rounding of one code may have done there.  2^f is the largest power of two <= the row's
 // largest p_j sv_j of the tile's 128 keys, so a term keeps 27 bits below the
 // largest one beside it: neither a V row of a large scale that this row does not
 // see or weigh, nor a key in another tile that draws most of the weight, takes
