@@ -9,6 +9,7 @@ _msa_torch.json beside it), and is built anew under others.
 """
 from __future__ import annotations
 
+import contextlib
 import glob
 import json
 import os
@@ -129,8 +130,8 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
-    if os.path.exists(BINDING_KEY):  # (the record never speaks for a module that it does not belong to)
-        os.remove(BINDING_KEY)
+    with contextlib.suppress(FileNotFoundError):
+        os.remove(BINDING_KEY)  # (it never speaks for a module that it does not belong to)
     os.replace(tmp, BINDING)
     with open(tmp, "w") as f:
         json.dump(key, f)
