@@ -45,15 +45,16 @@ msa_status check_cache(int Hkv, int d, int block, int num_pages) {
     return MSA_OK;
 }
 
+bool step_fits(int page_stride, int Bt, int total, int block) {
+    return static_cast<long long>(page_stride) * block < (1ll << 30) && total < (1 << 30) && Bt < (1 << 24);
+}
+
 msa_status check_step(const int32_t *page_table, int page_stride, const int32_t *cu,
                       const int32_t *kv_len, int Bt, int total, int block) {
     if (!page_table || !cu || !kv_len || page_stride < 1 || Bt < 1 || total < 0)
         return MSA_ERR_INVALID_ARG;
     if (!aligned4(page_table) || !aligned4(cu) || !aligned4(kv_len)) return MSA_ERR_INVALID_ARG;
-    if (static_cast<long long>(page_stride) * block >= (1ll << 30) || total >= (1 << 30) ||
-        Bt >= (1 << 24))
-        return MSA_ERR_UNSUPPORTED;
-    return MSA_OK;
+    return step_fits(page_stride, Bt, total, block) ? MSA_OK : MSA_ERR_UNSUPPORTED;
 }
 
 msa_status check_ws(const void *ws, size_t bytes, size_t need) {
@@ -349,8 +350,9 @@ msa_status msa_kv_gather_i8(const int8_t *k_pages, const int8_t *v_pages, const 
 
 int msa_attn_paged_kernels(int Bt, int total, int max_q, int Hq, int Hkv, int block,
                            int page_stride, int window, int sinks) {
-    if (Bt < 1 || total < 1 || max_q < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || block < 1 ||
-        page_stride < 1 || window < 0 || sinks < 0)
+    if (Bt < 1 || total < 1 || max_q < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || page_stride < 1 ||
+        window < 0 || sinks < 0 || check_cache(Hkv, 128, block, 1) != MSA_OK ||
+        !step_fits(page_stride, Bt, total, block) || static_cast<long long>(total) * Hq >= (1ll << 31))
         return 0;
     const Choice c = choose(Bt, total, known_rows(max_q, total), Hq / Hkv, Hkv,
                             static_cast<long long>(page_stride) * block, clamp_window(window),

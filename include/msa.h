@@ -337,8 +337,9 @@ MSA_API msa_status msa_attn_paged_i8(const void *q, int64_t q_stride, const int8
  * The kernels that msa_attn_paged and msa_attn_paged_i8 launch for a step of
  * these sizes (profiling and tests): MSA_KERNEL_SPLIT, MSA_KERNEL_CHUNK or both,
  * where the chunk kernel takes the sequences with more than 16 rows (n_b * Hq /
- * Hkv) and the split kernel the others; 0 for sizes without work or that the
- * calls reject.  Host only: no CUDA call is made.
+ * Hkv) and the split kernel the others; 0 for sizes without work or outside the
+ * limits above (but for that on triples, which depends on the device).  Host
+ * only: no CUDA call is made.
  */
 #define MSA_KERNEL_SPLIT 1
 #define MSA_KERNEL_CHUNK 2

@@ -29,6 +29,12 @@ def msa():
     ((1, 4, 8, 2, 64, 63, -1, 0, None), ()),
     ((1, 4, 8, 2, 64, 63, 0, -1, None), ()),
     ((1, 4, 8, 2, 64, 63, 0, 0, -1), ()),
+    ((1, 4, 8, 2, 48, 63, 0, 0, None), ()),                          # no such block
+    ((1, 2 ** 31 - 1, 2 ** 31 - 1, 1, 128, 2 ** 31 - 1, 0, 0, None), ()),
+    ((1, 64, 32, 8, 128, 2 ** 31 - 1, 0, 0, None), ()),
+    ((1, 2 ** 30, 1, 1, 128, 8, 0, 0, None), ()),
+    ((2 ** 24, 64, 32, 8, 128, 8, 0, 0, None), ()),
+    ((1, 2 ** 26, 32, 8, 128, 8, 0, 0, None), ()),
 ])
 def test_choice(msa, step, kernels):
     *sizes, max_q = step
